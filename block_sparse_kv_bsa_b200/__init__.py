@@ -17,6 +17,13 @@ The functions carry the C names:
 * :func:`bsa_route_qmean` - the same route from precomputed query means
 * :func:`bsa_attn` - indexed block-sparse attention (O and LSE)
 * :func:`bsa_attn_tokens` - the same with O and LSE in raster token order
+* :class:`Rope`, :func:`bsa_rope` - rotary positions on tokens, and their gradient
+* :func:`bsa_tokens_to_blocks_rope` / :func:`bsa_kv_append_rope` - the same on
+  the way into block order
+* :class:`KVCache8`, :func:`bsa_kv8_append` - a cache in e4m3 with one scale per
+  block and head
+* :func:`bsa_kv8_attn` / :func:`bsa_kv8_attn_decode` - attention over it, by query
+  blocks or by a few query tokens
 * :func:`bsa_check_device_error` - read and clear the device error word
 
 Method: "Velox: Spatial Memory Makes World Models Efficient" (Key
@@ -42,7 +49,8 @@ STATUS_NAMES = {
     4: "BSA_ERR_UNSUPPORTED", 5: "BSA_ERR_CUDA", 6: "BSA_ERR_DEVICE_FAULT", 7: "BSA_ERR_TIMEOUT",
 }
 DEV_CODES = {0: "BSA_DEV_OK", 1: "BSA_DEV_BAD_INDEX", 2: "BSA_DEV_BAD_COUNT",
-             3: "BSA_DEV_BAD_VALID", 4: "BSA_DEV_BAD_PERM", 5: "BSA_DEV_WAIT_TIMEOUT"}
+             3: "BSA_DEV_BAD_VALID", 4: "BSA_DEV_BAD_PERM", 5: "BSA_DEV_WAIT_TIMEOUT",
+             6: "BSA_DEV_BAD_SCALE"}
 
 # Every symbol include/bsa.h declares (checked by the tests).
 EXPORTS = ("bsa_abi_version", "bsa_status_string", "bsa_gilbert_perm", "bsa_kv_append",
@@ -52,6 +60,9 @@ EXPORTS = ("bsa_abi_version", "bsa_status_string", "bsa_gilbert_perm", "bsa_kv_a
            "bsa_route_velox_qmean",
            "bsa_route_noalloc", "bsa_attn", "bsa_attn_tokens",
            "bsa_geometry_prior",
+           "bsa_rope_frequencies", "bsa_rope_phases", "bsa_rope", "bsa_tokens_to_blocks_rope",
+           "bsa_kv_append_rope", "bsa_kv8_append", "bsa_kv8_attn",
+           "bsa_kv8_attn_decode_workspace_size", "bsa_kv8_attn_decode",
            "bsa_check_device_error",
            "bsa_selftest_bounded_wait")
 
@@ -91,6 +102,23 @@ class CVeloxRoute(ctypes.Structure):
                 ("ref_first", ctypes.c_int32), ("n_ref", ctypes.c_int32)]
 
 
+class CRope(ctypes.Structure):
+    """ctypes mirror of ``bsa_rope_desc``."""
+    _fields_ = [("phase", ctypes.c_void_p), ("n_pairs", ctypes.c_int32 * 3),
+                ("n_axes", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("pos", ctypes.c_void_p), ("origin", ctypes.c_int32 * 3)]
+
+
+class CCache8(ctypes.Structure):
+    """ctypes mirror of ``bsa_kv_cache8``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("block_valid", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("Hh", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+                ("kmean", ctypes.c_void_p)]
+
+
 _i, _p, _f, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_float, ctypes.c_size_t
 _sig = {
     "bsa_abi_version": (ctypes.c_int, []),
@@ -117,6 +145,21 @@ _sig = {
     "bsa_attn": (_i, [_p, ctypes.POINTER(CCache), _p, _p, _p, _i, _i, _f, _p, _p, _p, _p]),
     "bsa_attn_tokens": (_i, [_p, ctypes.POINTER(CCache), _p, _p, _p, _i, _f, _i, _i, _i, _p, _p,
                              _p, _p, _p]),
+    "bsa_rope_frequencies": (_i, [_i, ctypes.c_double, _i, ctypes.c_double, ctypes.c_double,
+                                  ctypes.c_double, ctypes.c_double, _p, _p]),
+    "bsa_rope_phases": (_i, [_p, _i, _p]),
+    "bsa_rope": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, ctypes.POINTER(CRope), _p]),
+    "bsa_tokens_to_blocks_rope": (_i, [_p, _p, _p, _i, _i, _i, _i, _i, _i, _p,
+                                       ctypes.POINTER(CRope), _p, _p]),
+    "bsa_kv_append_rope": (_i, [ctypes.POINTER(CCache), _p, _p, _i, _i, _i, _p,
+                                ctypes.POINTER(CRope), _p, _p]),
+    "bsa_kv8_append": (_i, [ctypes.POINTER(CCache8), _p, _p, _i, _i, _i, _p,
+                            ctypes.POINTER(CRope), _p, _p]),
+    "bsa_kv8_attn": (_i, [_p, ctypes.POINTER(CCache8), _i, _p, _p, _p, _i, _i, _f, _p, _p, _p,
+                          _p]),
+    "bsa_kv8_attn_decode_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "bsa_kv8_attn_decode": (_i, [_p, ctypes.POINTER(CCache8), _i, _i, _p, _p, _i, _f, _p, _p, _p,
+                                 _sz, _p, _p]),
     "bsa_check_device_error": (_i, [_p, _p, ctypes.POINTER(ctypes.c_int32)]),
     "bsa_selftest_bounded_wait": (_i, [_p, ctypes.c_longlong, _p]),
 }
@@ -612,6 +655,384 @@ def bsa_attn_tokens(q_blk: torch.Tensor, cache: KVCache, idx: torch.Tensor, cnt:
         _ptr(q_blk), ctypes.byref(cs), _ptr(q_valid), _ptr(idx), _ptr(cnt), int(max_sel),
         float(sm_scale), int(T), int(H), int(W), _ptr(perm), _ptr(o), _ptr(lse),
         _ptr(error_word(dev)), _stream(dev)))
+    return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def bsa_rope_frequencies(n_pairs: int, base: float = 10000.0, scaling: str = "none",
+                         factor: float = 1.0, original_length: float = 1.0,
+                         beta_fast: float = 32.0, beta_slow: float = 1.0
+                         ) -> Tuple[np.ndarray, float]:
+    """(frequencies in radians per position (host float64 [n_pairs]), amplitude)
+    of one axis; ``scaling`` is "none", "linear", "base" or "by_parts"."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
+    out = np.empty(max(int(n_pairs), 1), dtype=np.float64)
+    amp = ctypes.c_double(1.0)
+    _check("bsa_rope_frequencies", _lib.bsa_rope_frequencies(
+        int(n_pairs), float(base), ROPE_SCALINGS[scaling], float(factor), float(original_length),
+        float(beta_fast), float(beta_slow), out.ctypes.data_as(ctypes.c_void_p),
+        ctypes.byref(amp)))
+    return out[:int(n_pairs)], float(amp.value)
+
+
+def bsa_rope_phases(freqs) -> np.ndarray:
+    """Frequencies (radians per position) as 64-bit fractions of a turn (host int64)."""
+    f = np.ascontiguousarray(freqs, dtype=np.float64).reshape(-1)
+    out = np.empty(max(f.size, 1), dtype=np.int64)
+    _check("bsa_rope_phases", _lib.bsa_rope_phases(f.ctypes.data_as(ctypes.c_void_p), f.size,
+                                                    out.ctypes.data_as(ctypes.c_void_p)))
+    return out[:f.size]
+
+
+class Rope:
+    """Rotary positions: the phase table on a device, the pairs of each axis, the
+    layout and the amplitude.
+
+    ``pairs`` is (P,) for one position per token or (Pt, Ph, Pw) for the
+    (t, h, w) positions of a chunk's grid; every axis with its own frequencies
+    base^(-i / pairs of the axis), scaled as in :func:`bsa_rope_frequencies`."""
+
+    def __init__(self, pairs, layout: str = "interleaved", base: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original_length: float = 1.0,
+                 beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+        pairs = tuple(int(p) for p in pairs)
+        made = [bsa_rope_frequencies(p, base, scaling, factor, original_length, beta_fast,
+                                     beta_slow) for p in pairs if p > 0]
+        if not made:
+            raise ValueError("pairs must turn at least one pair")
+        self._set(np.concatenate([f for f, _ in made]), pairs, layout, made[0][1], device)
+
+    @classmethod
+    def from_frequencies(cls, freqs, pairs, layout: str = "interleaved", amplitude: float = 1.0,
+                         device="cuda") -> "Rope":
+        """From frequencies in radians per position, section by section."""
+        self = cls.__new__(cls)
+        self._set(freqs, pairs, layout, amplitude, device)
+        return self
+
+    def _set(self, freqs, pairs, layout, amplitude, device):
+        pairs = tuple(int(p) for p in pairs)
+        if len(pairs) not in (1, 3) or min(pairs) < 0:
+            raise ValueError("pairs must be (P,) or (Pt, Ph, Pw)")
+        if layout not in ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}")
+        phase = bsa_rope_phases(freqs)
+        if phase.size != sum(pairs):
+            raise ValueError(f"{phase.size} frequencies for {sum(pairs)} pairs")
+        self.pairs, self.layout, self.amplitude = pairs, layout, float(amplitude)
+        self.device = _dev(device)
+        self.phase = torch.from_numpy(phase).to(self.device)
+
+    @property
+    def n_axes(self) -> int:
+        return len(self.pairs)
+
+    def c_struct(self, B: int, N: int, pos: Optional[torch.Tensor], origin,
+                 inverse: bool = False) -> CRope:
+        if pos is not None:
+            _need(pos, "pos", torch.int32, self.device, (self.n_axes, B, N))
+        o = tuple(int(x) for x in origin)
+        if len(o) != 3 or not all(-(1 << 31) <= x < (1 << 31) for x in o):
+            raise ValueError("origin must be three int32 positions")
+        p = self.pairs + (0,) * (3 - len(self.pairs))
+        return CRope(self.phase.data_ptr(), (ctypes.c_int32 * 3)(*p), self.n_axes,
+                     ROPE_LAYOUTS[self.layout], int(bool(inverse)), self.amplitude,
+                     None if pos is None else pos.data_ptr(), (ctypes.c_int32 * 3)(*o))
+
+
+def _on(device, fn: str, *args):
+    """Call the library with ``device`` current."""
+    call = getattr(_lib, fn)
+    if device.index == torch.cuda.current_device():
+        _check(fn, call(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, call(*args))
+
+
+def _rope_struct(rope: Optional[Rope], dev, B, N, pos, origin, inverse=False):
+    if rope is None:
+        return None
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if rope.device != dev:
+        raise ValueError(f"rope is on {rope.device}, expected {dev}")
+    return ctypes.byref(rope.c_struct(B, N, pos, origin, inverse))
+
+
+def _perm_or_gilbert(perm: Optional[torch.Tensor], T: int, H: int, W: int, dev):
+    """The caller's slot table, or the Gilbert table, or (for chunks too large
+    for a table) None: the kernels then walk the curve."""
+    if perm is not None:
+        _need(perm, "perm", torch.int32, dev, (T * H * W,))
+        return perm
+    return gilbert_perm_device(T, H, W, dev) if T * H * W <= GATHER_MAX_TOKENS else None
+
+
+GATHER_MAX_TOKENS = 1 << 14
+
+
+def _tokens_shape(x: torch.Tensor, name: str, T: int, H: int, W: int):
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError(f"{name} must be [B, T*H*W, Hh, D]")
+    if x.shape[1] != T * H * W:
+        raise ValueError(f"{name} has {x.shape[1]} tokens, expected {T * H * W}")
+    _need(x, name, torch.bfloat16)
+    return x.shape
+
+
+def bsa_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope: Rope,
+             pos: Optional[torch.Tensor] = None, origin=(0, 0, 0), inverse: bool = False,
+             out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions of raster tokens (bf16 [B, T*H*W, Hh, D]); a sequence of
+    n tokens is T = n, H = W = 1.  ``pos`` (int32 [axes, B, T*H*W]) gives every
+    token's positions, otherwise the grid does; ``origin`` is added to both.
+    ``inverse`` turns back: the gradient of the call.  ``out`` may be x_tok."""
+    B, N, Hh, D = _tokens_shape(x_tok, "x_tok", T, H, W)
+    dev = x_tok.device
+    if out is None:
+        out = torch.empty_like(x_tok)
+    else:
+        _need(out, "out", torch.bfloat16, dev, x_tok.shape)
+    if rope is None:
+        raise TypeError("rope must be a Rope")
+    _on(dev, "bsa_rope", _ptr(x_tok), _ptr(out), B, Hh, D, int(T), int(H), int(W),
+        _rope_struct(rope, dev, B, N, pos, origin, inverse), _stream(dev))
+    return out
+
+
+def bsa_tokens_to_blocks_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope: Rope,
+                              pos: Optional[torch.Tensor] = None, origin=(0, 0, 0),
+                              out: Optional[torch.Tensor] = None,
+                              mean: Optional[torch.Tensor] = None, want_mean: bool = False,
+                              perm: Optional[torch.Tensor] = None):
+    """bsa_tokens_to_blocks of the turned tokens in one pass; returns the blocks,
+    or (blocks, means) with ``want_mean`` or a ``mean`` buffer.  ``perm`` (int32
+    [T*H*W], token -> slot) replaces the Gilbert order."""
+    B, N, Hh, D = _tokens_shape(x_tok, "x_tok", T, H, W)
+    dev = x_tok.device
+    nb = n_blocks_for(T, H, W)
+    if out is None:
+        out = torch.empty((B, Hh, nb * BLK, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(out, "out", torch.bfloat16, dev, (B, Hh, nb * BLK, D))
+    if mean is not None:
+        _need(mean, "mean", torch.float32, dev, (B, Hh, nb, D))
+    elif want_mean:
+        mean = torch.empty((B, Hh, nb, D), dtype=torch.float32, device=dev)
+    if rope is None:
+        raise TypeError("rope must be a Rope")
+    table = _perm_or_gilbert(perm, T, H, W, dev)
+    _on(dev, "bsa_tokens_to_blocks_rope", _ptr(x_tok), _ptr(out), _ptr(mean), B, Hh, D, int(T),
+        int(H), int(W), _ptr(table), _rope_struct(rope, dev, B, N, pos, origin),
+        _ptr(error_word(dev)), _stream(dev))
+    return out if mean is None else (out, mean)
+
+
+def bsa_kv_append_rope(cache: KVCache, k_tok: torch.Tensor, v_tok: torch.Tensor, T: int, H: int,
+                       W: int, rope: Rope, pos: Optional[torch.Tensor] = None, origin=(0, 0, 0),
+                       perm: Optional[torch.Tensor] = None) -> int:
+    """bsa_kv_append with the keys turned on the way; returns the first block."""
+    dev = cache.device
+    shape = (cache.B, T * H * W, cache.Hh, cache.D)
+    _need(k_tok, "k_tok", torch.bfloat16, dev, shape)
+    _need(v_tok, "v_tok", torch.bfloat16, dev, shape)
+    if rope is None:
+        raise TypeError("rope must be a Rope")
+    table = _perm_or_gilbert(perm, T, H, W, dev)
+    cs = cache.c_struct()
+    first = cache.n_blocks
+    _on(dev, "bsa_kv_append_rope", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), int(T), int(H),
+        int(W), _ptr(table), _rope_struct(rope, dev, cache.B, T * H * W, pos, origin),
+        _ptr(error_word(dev)), _stream(dev))
+    cache.n_blocks = int(cs.n_blocks)
+    return first
+
+
+# ---------------------------------------------------------------------------
+# 8-bit KV cache
+# ---------------------------------------------------------------------------
+
+class KVCache8:
+    """A caller-owned block KV cache in 8 bits: K, V e4m3 [B, Hh, max_blocks, 128,
+    D], one fp32 scale per (batch, head, block) for each, the valid-row counts,
+    and optionally the pooled keys.  The route calls take it as they take a
+    :class:`KVCache` with pooled keys (they read only those)."""
+
+    def __init__(self, B: int, Hh: int, D: int, max_blocks: int, device="cuda",
+                 pooled_keys: bool = False):
+        dev = _dev(device)
+        shape = (int(B), int(Hh), int(max_blocks), BLK, int(D))
+        self._set(torch.zeros(shape, dtype=torch.float8_e4m3fn, device=dev),
+                  torch.ones(shape[:3], dtype=torch.float32, device=dev),
+                  torch.zeros(shape, dtype=torch.float8_e4m3fn, device=dev),
+                  torch.ones(shape[:3], dtype=torch.float32, device=dev),
+                  torch.zeros(shape[2], dtype=torch.int32, device=dev), 0,
+                  torch.zeros(shape[:3] + shape[4:], dtype=torch.float32, device=dev)
+                  if pooled_keys else None)
+
+    @classmethod
+    def from_tensors(cls, k: torch.Tensor, k_scale: torch.Tensor, v: torch.Tensor,
+                     v_scale: torch.Tensor, block_valid: torch.Tensor, n_blocks: int,
+                     kmean: Optional[torch.Tensor] = None) -> "KVCache8":
+        """A cache over the caller's own tensors, ``n_blocks`` blocks of it in use."""
+        self = cls.__new__(cls)
+        self._set(k, k_scale, v, v_scale, block_valid, n_blocks, kmean)
+        return self
+
+    def _set(self, k, k_scale, v, v_scale, block_valid, n_blocks, kmean):
+        if not isinstance(k, torch.Tensor) or k.dim() != 5 or k.shape[3] != BLK:
+            raise ValueError("k must be [B, Hh, max_blocks, 128, D]")
+        B, Hh, nb, _, D = k.shape
+        _need(k, "k", torch.float8_e4m3fn)
+        _need(v, "v", torch.float8_e4m3fn, k.device, k.shape)
+        _need(k_scale, "k_scale", torch.float32, k.device, (B, Hh, nb))
+        _need(v_scale, "v_scale", torch.float32, k.device, (B, Hh, nb))
+        _need(block_valid, "block_valid", torch.int32, k.device, (nb,))
+        if kmean is not None:
+            _need(kmean, "kmean", torch.float32, k.device, (B, Hh, nb, D))
+        if not 0 <= int(n_blocks) <= nb:
+            raise ValueError(f"n_blocks must lie in [0, {nb}]")
+        self.k, self.k_scale, self.v, self.v_scale = k, k_scale, v, v_scale
+        self.block_valid, self.kmean = block_valid, kmean
+        self.B, self.Hh, self.D, self.max_blocks = B, Hh, D, nb
+        self.n_blocks, self.device = int(n_blocks), k.device
+
+    def c_struct(self) -> CCache:
+        """The route calls' view: pooled keys, no bf16 K or V."""
+        return CCache(None, None, self.block_valid.data_ptr(), self.B, self.Hh, self.D,
+                      self.max_blocks, self.n_blocks,
+                      None if self.kmean is None else self.kmean.data_ptr())
+
+    def c_struct8(self) -> CCache8:
+        return CCache8(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                       self.v_scale.data_ptr(), self.block_valid.data_ptr(), self.B, self.Hh,
+                       self.D, self.max_blocks, self.n_blocks,
+                       None if self.kmean is None else self.kmean.data_ptr())
+
+
+def _need_cache8(cache):
+    if not isinstance(cache, KVCache8):
+        raise TypeError("cache must be a KVCache8")
+
+
+def bsa_kv8_append(cache: KVCache8, k_tok: torch.Tensor, v_tok: torch.Tensor, T: int, H: int,
+                   W: int, rope: Optional[Rope] = None, pos: Optional[torch.Tensor] = None,
+                   origin=(0, 0, 0), perm: Optional[torch.Tensor] = None) -> int:
+    """Append one chunk (bf16 [B, T*H*W, Hh, D] K and V) to an 8-bit cache, the keys
+    turned on the way when ``rope`` is given; returns its first block."""
+    _need_cache8(cache)
+    dev = cache.device
+    shape = (cache.B, T * H * W, cache.Hh, cache.D)
+    _need(k_tok, "k_tok", torch.bfloat16, dev, shape)
+    _need(v_tok, "v_tok", torch.bfloat16, dev, shape)
+    table = _perm_or_gilbert(perm, T, H, W, dev)
+    cs = cache.c_struct8()
+    first = cache.n_blocks
+    _on(dev, "bsa_kv8_append", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), int(T), int(H), int(W),
+        _ptr(table), _rope_struct(rope, dev, cache.B, T * H * W, pos, origin),
+        _ptr(error_word(dev)), _stream(dev))
+    cache.n_blocks = int(cs.n_blocks)
+    return first
+
+
+def bsa_kv8_attn(q_blk: torch.Tensor, cache: KVCache8, idx: torch.Tensor, cnt: torch.Tensor,
+                 q_valid: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
+                 o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """bsa_attn over an 8-bit cache: q_blk bf16 [B, Hq, nQB*128, D] with Hq a multiple
+    of the cache's Hh, one route per cache head (idx [B, Hh, nQB, max_sel], cnt [B,
+    Hh, nQB]); returns (O like q_blk, LSE fp32 [B, Hq, nQB*128])."""
+    _need_cache8(cache)
+    dev = cache.device
+    if q_blk.dim() != 4:
+        raise ValueError("q_blk must be [B, Hq, nQB*128, D]")
+    B, Hq, R, D = q_blk.shape
+    if (B, D) != (cache.B, cache.D) or Hq % cache.Hh or Hq == 0 or R % BLK:
+        raise ValueError("q_blk does not match the cache")
+    nqb = R // BLK
+    _need(q_blk, "q_blk", torch.bfloat16, dev)
+    if idx.dim() != 4 or tuple(idx.shape[:3]) != (B, cache.Hh, nqb):
+        raise ValueError("idx must be [B, Hh, nQB, max_sel]")
+    _need(idx, "idx", torch.int32, dev)
+    _need(cnt, "cnt", torch.int32, dev, (B, cache.Hh, nqb))
+    if q_valid is not None:
+        _need(q_valid, "q_valid", torch.int32, dev, (nqb,))
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if o is None:
+        o = torch.empty_like(q_blk)
+    if lse is None:
+        lse = torch.empty((B, Hq, R), dtype=torch.float32, device=dev)
+    _need(o, "o", torch.bfloat16, dev, q_blk.shape)
+    _need(lse, "lse", torch.float32, dev, (B, Hq, R))
+    cs = cache.c_struct8()
+    _on(dev, "bsa_kv8_attn", _ptr(q_blk), ctypes.byref(cs), Hq, _ptr(q_valid), _ptr(idx),
+        _ptr(cnt), nqb, idx.shape[3], float(sm_scale), _ptr(o), _ptr(lse), _ptr(error_word(dev)),
+        _stream(dev))
+    return o, lse
+
+
+def bsa_kv8_attn_decode_workspace_size(B: int, Hq: int, Hh: int, D: int, n_tok: int,
+                                       n_sel: int) -> int:
+    """Bytes of workspace for routes of at most n_sel blocks (or n_sel blocks in use)."""
+    n = ctypes.c_size_t(0)
+    _check("bsa_kv8_attn_decode_workspace_size", _lib.bsa_kv8_attn_decode_workspace_size(
+        int(B), int(Hq), int(Hh), int(D), int(n_tok), int(n_sel), ctypes.byref(n)))
+    return int(n.value)
+
+
+def bsa_kv8_attn_decode(q_tok: torch.Tensor, cache: KVCache8, idx: Optional[torch.Tensor] = None,
+                        cnt: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None,
+                        o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None
+                        ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of a few query tokens (bf16 [B, n_tok, Hq, D], n_tok * Hq / Hh at most
+    128) over an 8-bit cache: over the blocks of one route per cache head (idx [B,
+    Hh, max_sel], cnt [B, Hh]), or over every block in use when both are None.
+    Returns (O like q_tok, LSE fp32 [B, n_tok, Hq])."""
+    _need_cache8(cache)
+    dev = cache.device
+    if q_tok.dim() != 4:
+        raise ValueError("q_tok must be [B, n_tok, Hq, D]")
+    B, n_tok, Hq, D = q_tok.shape
+    if (B, D) != (cache.B, cache.D) or Hq % cache.Hh or Hq == 0 or n_tok == 0:
+        raise ValueError("q_tok does not match the cache")
+    _need(q_tok, "q_tok", torch.bfloat16, dev)
+    if (idx is None) != (cnt is None):
+        raise ValueError("idx and cnt come together")
+    max_sel = 0
+    if idx is not None:
+        if idx.dim() != 3 or tuple(idx.shape[:2]) != (B, cache.Hh):
+            raise ValueError("idx must be [B, Hh, max_sel]")
+        _need(idx, "idx", torch.int32, dev)
+        _need(cnt, "cnt", torch.int32, dev, (B, cache.Hh))
+        max_sel = idx.shape[2]
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(D)
+    if o is None:
+        o = torch.empty_like(q_tok)
+    if lse is None:
+        lse = torch.empty((B, n_tok, Hq), dtype=torch.float32, device=dev)
+    _need(o, "o", torch.bfloat16, dev, q_tok.shape)
+    _need(lse, "lse", torch.float32, dev, (B, n_tok, Hq))
+    if workspace is None:
+        size = bsa_kv8_attn_decode_workspace_size(B, Hq, cache.Hh, D, n_tok,
+                                                  cache.n_blocks if idx is None else max_sel)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", torch.uint8, dev)
+    cs = cache.c_struct8()
+    _on(dev, "bsa_kv8_attn_decode", _ptr(q_tok), ctypes.byref(cs), Hq, n_tok, _ptr(idx), _ptr(cnt),
+        max_sel, float(sm_scale), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel(),
+        _ptr(error_word(dev)), _stream(dev))
     return o, lse
 
 

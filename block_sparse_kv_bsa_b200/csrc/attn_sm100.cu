@@ -697,7 +697,7 @@ static bool make_map(CUtensorMap* m, const void* base, long long rows, int D) {
   return r == CUDA_SUCCESS;
 }
 
-static bool device_is_sm100() {
+bool device_is_sm100() {
   int dev = 0, major = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)

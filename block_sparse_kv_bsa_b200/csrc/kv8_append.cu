@@ -1,0 +1,264 @@
+// kv8_append.cu - bsa_kv8_append: a chunk into the 8-bit cache.
+//
+// Per (batch, head, block) and tensor: A = max |r| over the block (r = the
+// turned key, or the value), scale = A / 448, code = e4m3(r * (448 / A)).  The
+// bytes it cannot do without are 2 read and 1 written per element.  A CTA
+// takes one block and a run of heads of one tensor; its 256 threads hold a
+// whole 128 x D tile in registers as bf16 (D/16 slots a row, rope.cuh), so
+// each element is read once: a first pass turns it and takes the maximum (and
+// the column sums of the keys), a second turns it again and rounds it.  The
+// angles belong to the row and are computed once for all heads of the run.
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "rope.cuh"
+#include "slots.cuh"
+
+namespace bsa {
+
+bsa_status check_rope_chunk(int B, int Hh, int D, int T, int H, int W);
+
+constexpr int kApp8Threads = 256;
+
+struct Append8Args {
+  RopeArgs rope;
+  const uint4* src[2];
+  uint8_t* dst[2];
+  float* scale[2];
+  float* kmean;         // optional
+  const int32_t* perm;
+  int32_t* block_valid;
+  int32_t* d_err;
+  int N, Hh, heads;
+  int max_blocks, base_block;
+  int T, H, W;
+};
+
+__device__ __forceinline__ float finite_abs(float x) {
+  x = fabsf(x);
+  return x <= 3.402823466e38f ? x : 0.f;  // infinities and NaN do not set the scale
+}
+
+template <int D, int MODE, bool kMean>
+__device__ __forceinline__ void append8_heads(const Append8Args& a, int which, int b, int h0,
+                                              int h1, const int* s_tok, int valid, float* s_red,
+                                              float* s_sum) {
+  constexpr int kSlots = D / 16, kVecs = D / 8;
+  constexpr int kRowStep = kApp8Threads / kSlots;
+  constexpr int kRows = kBlk / kRowStep;  // rows per thread
+  const int slot = threadIdx.x % kSlots;
+  const int row0 = threadIdx.x / kSlots;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long bN = static_cast<long long>(b) * a.N;
+  int va, vb;
+  slot_vectors<MODE>(a.rope.P, slot, va, vb);
+  SlotTrig g[kRows];
+  int tok[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    tok[i] = s_tok[row0 + i * kRowStep];
+    if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
+      slot_trig<MODE>(a.rope, token_pos(a.rope, bN, max(tok[i], 0)), slot, g[i]);
+      if (tok[i] < 0) g[i].n = 0;  // pad rows stay +0
+    }
+  }
+  const uint4* src = a.src[which];
+  for (int h = h0; h < h1; ++h) {
+    const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block +
+                          blockIdx.x;
+    uint4 x[kRows], y[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      if (MODE != kRopeHalfAny && tok[i] >= 0) {
+        const uint4* row = src + ((bN + tok[i]) * a.Hh + h) * kVecs;
+        x[i] = ld_nc_v4(row + va);
+        y[i] = ld_nc_v4(row + vb);
+      }
+    }
+    auto value = [&](int i, float(&p)[8], float(&q)[8]) {
+      if (MODE == kRopeHalfAny) {
+        if (tok[i] >= 0) {
+          turn_slot_any(a.rope, token_pos(a.rope, bN, tok[i]), slot,
+                        reinterpret_cast<const __nv_bfloat16*>(
+                            src + ((bN + tok[i]) * a.Hh + h) * kVecs), p, q);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
+        }
+        return;
+      }
+      unpack8(x[i], p);
+      unpack8(y[i], q);
+      if (MODE != kRopeNone) turn_slot<MODE>(g[i], p, q);
+    };
+    float amax = 0.f;
+    float sum[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float p[8], q[8];
+      value(i, p, q);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        amax = fmaxf(amax, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
+        if (kMean) {
+          sum[e] += p[e];
+          sum[8 + e] += q[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    if (kMean) {
+      // Lanes with the same slot hold the same columns.
+#pragma unroll
+      for (int off = kSlots; off < 32; off <<= 1) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], off);
+      }
+    }
+    __syncthreads();  // the previous head's reads of s_red and s_sum are done
+    if (lane == 0) s_red[warp] = amax;
+    if (kMean && lane < kSlots) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s_sum[warp * D + va * 8 + e] = sum[e];
+        s_sum[warp * D + vb * 8 + e] = sum[8 + e];
+      }
+    }
+    __syncthreads();
+    amax = s_red[0];
+#pragma unroll
+    for (int w = 1; w < kApp8Threads / 32; ++w) amax = fmaxf(amax, s_red[w]);
+    amax = fmaxf(amax, kAmaxFloor);
+    const float mul = kE4m3Max / amax;
+    if (threadIdx.x == 0) a.scale[which][blk] = amax / kE4m3Max;
+    if (kMean) {
+      for (int c = threadIdx.x; c < D; c += kApp8Threads) {
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kApp8Threads / 32; ++w) t += s_sum[w * D + c];
+        a.kmean[blk * D + c] = t / static_cast<float>(valid);
+      }
+    }
+    uint8_t* dst = a.dst[which] + blk * (kBlk * D);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      float p[8], q[8];
+      value(i, p, q);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        w[e] = pack_e4m3x2(p[4 * e] * mul, p[4 * e + 1] * mul) |
+               (pack_e4m3x2(p[4 * e + 2] * mul, p[4 * e + 3] * mul) << 16);
+        w[2 + e] = pack_e4m3x2(q[4 * e] * mul, q[4 * e + 1] * mul) |
+                   (pack_e4m3x2(q[4 * e + 2] * mul, q[4 * e + 3] * mul) << 16);
+      }
+      uint8_t* row = dst + (row0 + i * kRowStep) * D;
+      if (MODE == kRopeHalf) {
+        *reinterpret_cast<uint2*>(row + va * 8) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(row + vb * 8) = make_uint2(w[2], w[3]);
+      } else {  // the two vectors are neighbours
+        st_v4(row + va * 8, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+  }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kApp8Threads)
+append8_kernel(Append8Args a) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  __shared__ int s_tok[kBlk];
+  __shared__ float s_red[kApp8Threads / 32];
+  __shared__ float s_sum[kApp8Threads / 32 * D];
+  const int j = blockIdx.x;
+  const int b = blockIdx.z / 2, which = blockIdx.z % 2;
+  const int slot0 = j * kBlk;
+  const int valid = min(kBlk, a.N - slot0);
+  const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
+  invert_block_slots<kApp8Threads>(a.perm, a.N, slot0, s_tok, j == 0 && first_cta, a.d_err, a.T,
+                                   a.H, a.W);
+  if (first_cta && threadIdx.x == 0) a.block_valid[a.base_block + j] = valid;
+  // A slot of the chunk that no token maps to: perm is not a permutation.
+  if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
+  const int h0 = blockIdx.y * a.heads;
+  const int h1 = min(h0 + a.heads, a.Hh);
+  if (which == 1) {
+    append8_heads<D, kRopeNone, false>(a, 1, b, h0, h1, s_tok, valid, s_red, s_sum);
+  } else if (a.kmean != nullptr) {
+    append8_heads<D, MODE, true>(a, 0, b, h0, h1, s_tok, valid, s_red, s_sum);
+  } else {
+    append8_heads<D, MODE, false>(a, 0, b, h0, h1, s_tok, valid, s_red, s_sum);
+  }
+}
+
+template <int D>
+static bsa_status launch_append8(int mode, const Append8Args& a, int B, int nb, cudaStream_t s) {
+  dim3 grid(nb, (a.Hh + a.heads - 1) / a.heads, 2 * B);
+  const dim3 block(kApp8Threads);
+  switch (mode) {
+    case kRopeNone: return launch_pdl(append8_kernel<D, kRopeNone>, grid, block, 0, s, a);
+    case kRopeInterleaved:
+      return launch_pdl(append8_kernel<D, kRopeInterleaved>, grid, block, 0, s, a);
+    case kRopeHalf: return launch_pdl(append8_kernel<D, kRopeHalf>, grid, block, 0, s, a);
+    default: return launch_pdl(append8_kernel<D, kRopeHalfAny>, grid, block, 0, s, a);
+  }
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" bsa_status bsa_kv8_append(bsa_kv_cache8* c, const void* k_tok, const void* v_tok, int T,
+                                     int H, int W, const int32_t* d_perm,
+                                     const bsa_rope_desc* rope, int32_t* d_err, void* stream) {
+  if (c == nullptr || k_tok == nullptr || v_tok == nullptr || c->k == nullptr ||
+      c->v == nullptr || c->k_scale == nullptr || c->v_scale == nullptr ||
+      c->block_valid == nullptr)
+    return BSA_ERR_INVALID_ARG;
+  BSA_TRY(check_rope_chunk(c->B, c->Hh, c->D, T, H, W));
+  if (!aligned16(k_tok) || !aligned16(v_tok) || !aligned16(c->k) || !aligned16(c->v) ||
+      !aligned16(c->kmean))
+    return BSA_ERR_INVALID_ARG;
+  if (c->max_blocks <= 0 || c->n_blocks < 0 || c->n_blocks > c->max_blocks)
+    return BSA_ERR_INVALID_ARG;
+  Append8Args a{};
+  int mode = kRopeNone;
+  if (rope != nullptr) BSA_TRY(rope_args(rope, c->B, c->D, T, H, W, &a.rope, &mode));
+  const int n = T * H * W;
+  if (d_perm != nullptr && n > kGatherMaxTokens) return BSA_ERR_UNSUPPORTED;
+  const int nb = (n + kBlk - 1) / kBlk;
+  if (nb > c->max_blocks - c->n_blocks) return BSA_ERR_CAPACITY;
+  a.src[0] = static_cast<const uint4*>(k_tok);
+  a.src[1] = static_cast<const uint4*>(v_tok);
+  a.dst[0] = static_cast<uint8_t*>(c->k);
+  a.dst[1] = static_cast<uint8_t*>(c->v);
+  a.scale[0] = c->k_scale;
+  a.scale[1] = c->v_scale;
+  a.kmean = c->kmean;
+  a.perm = d_perm;
+  a.block_valid = c->block_valid;
+  a.d_err = d_err;
+  a.N = n;
+  a.Hh = c->Hh;
+  // Two CTAs of this size fit an SM: enough of them for four waves, then as
+  // many heads as possible for each set of angles.
+  const long long others = 2LL * nb * c->B;
+  long long groups = (148 * 4 + others - 1) / others;
+  groups = groups > c->Hh ? c->Hh : groups;
+  a.heads = static_cast<int>((c->Hh + groups - 1) / groups);
+  a.max_blocks = c->max_blocks;
+  a.base_block = c->n_blocks;
+  a.T = T;
+  a.H = H;
+  a.W = W;
+  cudaStream_t s = as_stream(stream);
+  BSA_TRY(c->D == 128 ? launch_append8<128>(mode, a, c->B, nb, s)
+                      : launch_append8<64>(mode, a, c->B, nb, s));
+  c->n_blocks += nb;
+  return BSA_OK;
+}

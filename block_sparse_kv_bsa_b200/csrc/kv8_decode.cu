@@ -1,0 +1,347 @@
+// kv8_decode.cu - bsa_kv8_attn_decode: a few query tokens over the 8-bit
+// cache.
+//
+// The rows of one cache head are its n_tok * group query rows, 16 to a tile
+// (mma.sync, attn8_warp.cuh).  With so few rows the call is bound by reading
+// the cache once (1 byte an element of K and V), so the blocks are split over
+// enough CTAs to fill the GPU; each warp of a CTA streams its own 16-key
+// steps with the next step's loads in flight, the warps join through shared
+// memory and the splits through a workspace and a second small kernel, always
+// in the same order.
+#include "common.cuh"
+#include "attn8_warp.cuh"
+
+namespace bsa {
+
+bool device_is_sm100();
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = kDecWarps * 32;
+constexpr int kDecSlots = 296;     // CTAs resident at once: two on each of 148 SMs
+constexpr int kDecMaxRows = 128;   // query rows of one cache head
+constexpr int kDecChunk = kDecThreads;  // blocks whose metadata is staged at a time
+
+struct Decode8Args {
+  const __nv_bfloat16* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_valid;
+  const int32_t* idx;
+  const int32_t* cnt;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part_o;   // [B*Hh*tiles][n_split][16][D]
+  float* part_ml;  // [B*Hh*tiles][n_split][16][2]
+  int32_t* d_err;
+  int Hq, Hh, group, n_tok, rows, tiles, n_split;
+  int n_sel, max_blocks, n_blocks;
+  float scale_log2;
+};
+
+// Row r (token r / group, head r % group of the group) of cache head bh, as an
+// index of [B, n_tok, Hq].
+__device__ __forceinline__ long long query_row(const Decode8Args& a, long long bh, int r) {
+  const long long b = bh / a.Hh;
+  const int h = static_cast<int>(bh % a.Hh);
+  return (b * a.n_tok + r / a.group) * a.Hq + h * a.group + r % a.group;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kDecThreads, 2)
+decode8_kernel(Decode8Args a) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  using W = AttnWarp<D>;
+  __shared__ int s_blk[kDecChunk];
+  __shared__ int s_valid[kDecChunk];
+  __shared__ float s_ks[kDecChunk], s_vlog2[kDecChunk], s_vinv[kDecChunk];
+  __shared__ float s_o[kDecWarps][16][D];
+  __shared__ float s_ml[kDecWarps][16][2];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int split = blockIdx.y;
+  const long long item = blockIdx.x;
+  const long long bh = item / a.tiles;
+  const int tile = static_cast<int>(item % a.tiles);
+  const int r0 = tile * 16 + g;
+
+  W w;
+  w.init();
+  w.load_q(r0 < a.rows ? a.q + query_row(a, bh, r0) * D : nullptr,
+           r0 + 8 < a.rows ? a.q + query_row(a, bh, r0 + 8) * D : nullptr, a.scale_log2);
+
+  int n = a.n_sel;
+  if (a.cnt != nullptr) {
+    n = a.cnt[bh];
+    if (n < 0 || n > a.n_sel) {
+      report(a.d_err, BSA_DEV_BAD_COUNT);
+      n = n < 0 ? 0 : a.n_sel;
+    }
+  }
+  const int per = (n + a.n_split - 1) / a.n_split;
+  const int e0 = min(n, split * per), e1 = min(n, e0 + per);
+  for (int c0 = e0; c0 < e1; c0 += kDecChunk) {
+    const int count = min(kDecChunk, e1 - c0);
+    __syncthreads();
+    if (threadIdx.x < count) {
+      int blk = c0 + threadIdx.x;
+      if (a.idx != nullptr) {
+        blk = a.idx[bh * a.n_sel + blk];
+        if (blk < 0 || blk >= a.n_blocks) {
+          report(a.d_err, BSA_DEV_BAD_INDEX);
+          blk = 0;
+        }
+      }
+      int valid = a.block_valid[blk];
+      if (valid < 1 || valid > kBlk) {
+        report(a.d_err, BSA_DEV_BAD_VALID);
+        valid = valid < 1 ? 1 : kBlk;
+      }
+      const long long at = bh * a.max_blocks + blk;
+      const float vs = checked_scale(a.v_scale[at], a.d_err);
+      s_blk[threadIdx.x] = blk;
+      s_valid[threadIdx.x] = valid;
+      s_ks[threadIdx.x] = checked_scale(a.k_scale[at], a.d_err);
+      s_vlog2[threadIdx.x] = log2f(vs);
+      s_vinv[threadIdx.x] = 1.f / vs;
+    }
+    __syncthreads();
+    // Step u: keys (u % 8) * 16 .. of entry u / 8.
+    const int units = count * 8;
+    auto load = [&](int u, typename W::Keys& x) {
+      const long long at = (bh * a.max_blocks + s_blk[u / 8]) * (kBlk * D);
+      w.load_keys(a.k + at, a.v + at, (u % 8) * 16, s_valid[u / 8], x);
+    };
+    typename W::Keys cur, next;
+    if (warp < units) load(warp, cur);
+    for (int u = warp; u < units; u += kDecWarps) {
+      if (u + kDecWarps < units) load(u + kDecWarps, next);
+      const int e = u / 8;
+      if ((u % 8) * 16 < s_valid[e])
+        w.step(cur, (u % 8) * 16, s_valid[e], s_ks[e], s_vlog2[e], s_vinv[e]);
+      cur = next;
+    }
+  }
+  w.finish();
+
+  // Join the warps.
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+#pragma unroll
+    for (int i = 0; i < W::kTiles; ++i) {
+      s_o[warp][g + 8 * r][(2 * t) * (D / 8) + i] = w.o[i][2 * r];
+      s_o[warp][g + 8 * r][(2 * t + 1) * (D / 8) + i] = w.o[i][2 * r + 1];
+    }
+    if (t == 0) {
+      s_ml[warp][g + 8 * r][0] = w.m[r];
+      s_ml[warp][g + 8 * r][1] = w.l[r];
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * D; i += kDecThreads) {
+    const int r = i / D, d = i % D;
+    const int row = tile * 16 + r;
+    if (row >= a.rows) break;
+    float m = s_ml[0][r][0];
+#pragma unroll
+    for (int k = 1; k < kDecWarps; ++k) m = fmaxf(m, s_ml[k][r][0]);
+    float l = 0.f, o = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDecWarps; ++k) {
+      const float f = s_ml[k][r][0] == -INFINITY ? 0.f : ex2_approx(s_ml[k][r][0] - m);
+      l = fmaf(s_ml[k][r][1], f, l);
+      o = fmaf(s_o[k][r][d], f, o);
+    }
+    if (a.n_split == 1) {
+      const bool have = m > -INFINITY;
+      const long long out = query_row(a, bh, row);
+      a.o[out * D + d] = __float2bfloat16(have ? o / l : 0.f);
+      if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    } else {
+      const long long p = (item * a.n_split + split) * 16 + r;
+      a.part_o[p * D + d] = o;
+      if (d == 0) {
+        a.part_ml[p * 2] = m;
+        a.part_ml[p * 2 + 1] = l;
+      }
+    }
+  }
+}
+
+// Joins the splits of one query row.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+decode8_join_kernel(Decode8Args a) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  __shared__ float s_w[kDecSlots];
+  __shared__ float s_red[2][kJoinThreads / 32];
+  __shared__ float s_acc[kJoinThreads];
+  const int row = blockIdx.y;
+  const long long bh = blockIdx.x;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long p0 = (bh * a.tiles + row / 16) * a.n_split * 16 + row % 16;
+  float m = -INFINITY;
+  for (int s = threadIdx.x; s < a.n_split; s += kJoinThreads)
+    m = fmaxf(m, a.part_ml[(p0 + s * 16) * 2]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane == 0) s_red[0][warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, s_red[0][k]);
+  float l = 0.f;
+  for (int s = threadIdx.x; s < a.n_split; s += kJoinThreads) {
+    const float ms = a.part_ml[(p0 + s * 16) * 2];
+    const float f = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
+    s_w[s] = f;
+    l = fmaf(a.part_ml[(p0 + s * 16) * 2 + 1], f, l);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  if (lane == 0) s_red[1][warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) l += s_red[1][k];
+  constexpr int kGroups = kJoinThreads / D;
+  const int d = threadIdx.x % D, grp = threadIdx.x / D;
+  float acc = 0.f;
+#pragma unroll 8
+  for (int s = grp; s < a.n_split; s += kGroups)
+    acc = fmaf(a.part_o[(p0 + s * 16) * D + d], s_w[s], acc);
+  s_acc[threadIdx.x] = acc;
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int k = 1; k < kGroups; ++k) acc += s_acc[k * D + d];
+  const bool have = m > -INFINITY;
+  const long long out = query_row(a, bh, row);
+  a.o[out * D + d] = __float2bfloat16(have ? acc / l : 0.f);
+  if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Splits of n_sel blocks: the count whose waves over the resident CTAs leave
+// the fewest idle (a split is a wave's share of the blocks), fewest first.
+static int most_splits(long long items, int n_sel) {
+  long long most = kDecSlots / items;
+  if (most < 8) most = 8;
+  return static_cast<int>(most < n_sel ? most : n_sel);
+}
+
+static int split_count(long long items, int n_sel) {
+  const int most = most_splits(items, n_sel);
+  int best = 1;
+  double best_cost = 1e30;
+  for (int n = 1; n <= most; ++n) {
+    const long long waves = (items * n + kDecSlots - 1) / kDecSlots;
+    const double cost = static_cast<double>(waves) * ((n_sel + n - 1) / n) * (1.0 + 0.0001 * n);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+struct DecodeShape {
+  int rows, tiles, n_split;
+  size_t o_bytes, bytes;
+};
+
+static bsa_status decode_shape(int B, int Hq, int Hh, int D, int n_tok, int n_sel,
+                               DecodeShape* out) {
+  if (B <= 0 || Hq <= 0 || Hh <= 0 || n_tok <= 0 || n_sel < 0) return BSA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
+  if (Hq % Hh != 0) return BSA_ERR_SHAPE;
+  const long long rows = static_cast<long long>(n_tok) * (Hq / Hh);
+  if (rows > kDecMaxRows) return BSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * Hh > (1 << 20)) return BSA_ERR_SHAPE;
+  out->rows = static_cast<int>(rows);
+  out->tiles = (out->rows + 15) / 16;
+  const long long items = static_cast<long long>(B) * Hh * out->tiles;
+  out->n_split = n_sel > 0 ? split_count(items, n_sel) : 1;
+  // Sized for the most splits of any smaller n_sel: a program sizes the
+  // workspace once for the cache it will grow to.
+  const int most = most_splits(items, n_sel);
+  const size_t parts = most > 1 ? static_cast<size_t>(items) * most * 16 : 0;
+  out->o_bytes = (parts * D * sizeof(float) + 255) & ~static_cast<size_t>(255);
+  out->bytes = out->o_bytes + ((parts * 2 * sizeof(float) + 255) & ~static_cast<size_t>(255));
+  return BSA_OK;
+}
+
+template <int D>
+static bsa_status launch_decode(const Decode8Args& a, long long bh, cudaStream_t s) {
+  const long long items = bh * a.tiles;
+  BSA_TRY(launch_pdl(decode8_kernel<D>, dim3(static_cast<unsigned>(items), a.n_split),
+                     dim3(kDecThreads), 0, s, a));
+  if (a.n_split == 1) return BSA_OK;
+  return launch_pdl(decode8_join_kernel<D>, dim3(static_cast<unsigned>(bh), a.rows),
+                    dim3(kJoinThreads), 0, s, a);
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" bsa_status bsa_kv8_attn_decode_workspace_size(int B, int Hq, int Hh, int D, int n_tok,
+                                                         int n_sel, size_t* bytes) {
+  if (bytes == nullptr) return BSA_ERR_INVALID_ARG;
+  DecodeShape sh;
+  BSA_TRY(decode_shape(B, Hq, Hh, D, n_tok, n_sel, &sh));
+  *bytes = sh.bytes;
+  return BSA_OK;
+}
+
+extern "C" bsa_status bsa_kv8_attn_decode(const void* q_tok, const bsa_kv_cache8* c, int Hq,
+                                          int n_tok, const int32_t* idx, const int32_t* cnt,
+                                          int max_sel, float sm_scale, void* o_tok, float* lse,
+                                          void* workspace, size_t ws_bytes, int32_t* d_err,
+                                          void* stream) {
+  if (q_tok == nullptr || c == nullptr || o_tok == nullptr || lse == nullptr || c->k == nullptr ||
+      c->v == nullptr || c->block_valid == nullptr || c->k_scale == nullptr ||
+      c->v_scale == nullptr || (idx == nullptr) != (cnt == nullptr))
+    return BSA_ERR_INVALID_ARG;
+  if (c->B <= 0 || c->Hh <= 0 || c->max_blocks <= 0 || c->n_blocks < 0 ||
+      c->n_blocks > c->max_blocks || (idx != nullptr && max_sel <= 0) || !(sm_scale == sm_scale))
+    return BSA_ERR_INVALID_ARG;
+  if (!aligned16(q_tok) || !aligned16(c->k) || !aligned16(c->v) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return BSA_ERR_INVALID_ARG;
+  const int n_sel = idx != nullptr ? max_sel : c->n_blocks;
+  DecodeShape sh;
+  BSA_TRY(decode_shape(c->B, Hq, c->Hh, c->D, n_tok, n_sel, &sh));
+  if (sh.bytes > 0 && (workspace == nullptr || ws_bytes < sh.bytes)) return BSA_ERR_CAPACITY;
+  if (!device_is_sm100()) return BSA_ERR_UNSUPPORTED;
+  Decode8Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q_tok);
+  a.k = static_cast<const uint8_t*>(c->k);
+  a.v = static_cast<const uint8_t*>(c->v);
+  a.k_scale = c->k_scale;
+  a.v_scale = c->v_scale;
+  a.block_valid = c->block_valid;
+  a.idx = idx;
+  a.cnt = cnt;
+  a.o = static_cast<__nv_bfloat16*>(o_tok);
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + sh.o_bytes);
+  a.d_err = d_err;
+  a.Hq = Hq;
+  a.Hh = c->Hh;
+  a.group = Hq / c->Hh;
+  a.n_tok = n_tok;
+  a.rows = sh.rows;
+  a.tiles = sh.tiles;
+  a.n_split = sh.n_split;
+  a.n_sel = n_sel;
+  a.max_blocks = c->max_blocks;
+  a.n_blocks = c->n_blocks;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  const long long bh = static_cast<long long>(c->B) * c->Hh;
+  return c->D == 128 ? launch_decode<128>(a, bh, as_stream(stream))
+                     : launch_decode<64>(a, bh, as_stream(stream));
+}

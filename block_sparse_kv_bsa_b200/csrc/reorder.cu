@@ -16,13 +16,9 @@
 #include "common.cuh"
 #include "gilbert.cuh"
 #include "pool.cuh"
+#include "slots.cuh"
 
 namespace bsa {
-
-// The curve walk kept out of line: the kernels' table path stays compact.
-__device__ __noinline__ int curve_token_call(int T, int H, int W, int p) {
-  return curve_token(T, H, W, p);
-}
 
 constexpr int kRowsPerCta = 32;
 constexpr int kHeadsPerCta = 8;
@@ -185,7 +181,7 @@ block_mean_kernel(const uint4* kc, const int32_t* block_valid, float* kmean, int
   }
 }
 
-static bsa_status launch_block_means(const bsa_kv_cache* c, int first, int count, int32_t* d_err,
+bsa_status launch_block_means(const bsa_kv_cache* c, int first, int count, int32_t* d_err,
                                      cudaStream_t s) {
   if (count <= 0) return BSA_OK;
   dim3 grid((count + kMeanWarps - 1) / kMeanWarps, c->Hh, c->B);
@@ -199,78 +195,35 @@ static bsa_status launch_block_means(const bsa_kv_cache* c, int first, int count
   return launch_status();
 }
 
-// Slot -> token for the 128 curve slots [slot0, slot0 + 128) of one block:
-// s_tok[d] is the raster token whose perm entry is slot0 + d, or -1.  The
-// CTA's NT threads (NT >= 128) scan perm in rounds of kScan independent loads
-// per thread (one L2 round trip per round); entries outside [0, N) are
-// skipped, and reported when `report_bad`.  Ends with a CTA barrier.
-// s_tok[d] = the token at curve slot slot0 + d (d < 128), or -1 for a pad
-// slot.  With a table, the CTA scans perm (token -> slot); without one
-// (perm == NULL), each thread locates its slot on the curve.
-template <int NT>
-__device__ __forceinline__ void invert_block_slots(const int32_t* perm, int N, int slot0,
-                                                   int* s_tok, bool report_bad, int32_t* d_err,
-                                                   int T, int H, int W) {
-  static_assert(NT >= kBlk, "one thread per slot clears the table");
-  if (perm == nullptr) {
-    if (threadIdx.x < kBlk) {
-      const int p = slot0 + static_cast<int>(threadIdx.x);
-      s_tok[threadIdx.x] = p < N ? curve_token_call(T, H, W, p) : -1;
-    }
-    __syncthreads();
-    return;
+// The same for one tensor already in block order (nb blocks of N tokens).
+template <int VPR>
+__global__ void __launch_bounds__(kMeanWarps * 32)
+rows_mean_kernel(const uint4* x, float* mean, int Hh, int nb, int N) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  constexpr int D = VPR * 8;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = blockIdx.x * kMeanWarps + warp;
+  if (n >= nb) return;
+  const long long blk = (static_cast<long long>(blockIdx.z) * Hh + blockIdx.y) * nb + n;
+  const int c = lane % VPR, g = lane / VPR;
+  float km[8];
+  warp_block_mean<VPR>(x + blk * kBlk * VPR, min(kBlk, N - n * kBlk), c, g, km);
+  if (g == 0) {
+    float4* out = reinterpret_cast<float4*>(mean + blk * D + c * 8);
+    out[0] = make_float4(km[0], km[1], km[2], km[3]);
+    out[1] = make_float4(km[4], km[5], km[6], km[7]);
   }
-  if (threadIdx.x < kBlk) s_tok[threadIdx.x] = -1;
-  __syncthreads();
-  auto take = [&](int r, int p) {
-    if (p < 0 || p >= N) {
-      if (report_bad) report(d_err, BSA_DEV_BAD_PERM);
-      return;
-    }
-    const unsigned d = static_cast<unsigned>(p - slot0);
-    if (d < static_cast<unsigned>(kBlk)) s_tok[d] = r;
-  };
-  constexpr int kScan = 16;
-  // Four entries per load when perm is 16-byte aligned: one round of loads
-  // covers 64 * NT tokens, so a chunk's scan costs one memory latency.
-  int done = 0;
-  if ((reinterpret_cast<uintptr_t>(perm) & 15u) == 0) {
-    const int n4 = N / 4;
-    const int4* perm4 = reinterpret_cast<const int4*>(perm);
-    for (int base = 0; base < n4; base += kScan * NT) {
-      int4 pv[kScan];
-#pragma unroll
-      for (int k = 0; k < kScan; ++k) {
-        const int i = base + threadIdx.x + k * NT;
-        pv[k] = i < n4 ? __ldg(perm4 + i) : make_int4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < kScan; ++k) {
-        const int i = base + threadIdx.x + k * NT;
-        if (i >= n4) break;
-        take(4 * i, pv[k].x);
-        take(4 * i + 1, pv[k].y);
-        take(4 * i + 2, pv[k].z);
-        take(4 * i + 3, pv[k].w);
-      }
-    }
-    done = 4 * n4;
-  }
-  for (int base = done; base < N; base += kScan * NT) {
-    int pv[kScan];
-#pragma unroll
-    for (int k = 0; k < kScan; ++k) {
-      const int r = base + threadIdx.x + k * NT;
-      pv[k] = r < N ? __ldg(perm + r) : 0;
-    }
-#pragma unroll
-    for (int k = 0; k < kScan; ++k) {
-      const int r = base + threadIdx.x + k * NT;
-      if (r >= N) break;
-      take(r, pv[k]);
-    }
-  }
-  __syncthreads();
+}
+
+bsa_status launch_rows_mean(const void* x_blk, float* x_mean, int B, int Hh, int D, int nb, int N,
+                            cudaStream_t s) {
+  dim3 grid((nb + kMeanWarps - 1) / kMeanWarps, Hh, B);
+  const uint4* x = static_cast<const uint4*>(x_blk);
+  if (D == 128)
+    return launch_pdl(rows_mean_kernel<16>, grid, dim3(kMeanWarps * 32), 0, s, x, x_mean, Hh, nb,
+                      N);
+  return launch_pdl(rows_mean_kernel<8>, grid, dim3(kMeanWarps * 32), 0, s, x, x_mean, Hh, nb, N);
 }
 
 // Fused append for chunks of up to kGatherMaxTokens tokens: one CTA per
@@ -282,7 +235,6 @@ __device__ __forceinline__ void invert_block_slots(const int32_t* perm, int N, i
 // own slots by scanning it (perm is small and L2-resident at these sizes).
 constexpr int kAppendHeads = 4;
 constexpr int kAppendThreads = 2 * kAppendHeads * 32;  // K warps, then V warps
-constexpr int kGatherMaxTokens = 1 << 14;
 
 struct AppendArgs {
   const uint4* k_tok;

@@ -1,0 +1,391 @@
+// rope.cu - rotary positions: on raster tokens (bsa_rope, forward and
+// gradient) and on the way into 128-token blocks (bsa_tokens_to_blocks_rope,
+// bsa_kv_append_rope), with the host tables (bsa_rope_frequencies,
+// bsa_rope_phases).
+//
+// Both kernels are HBM streams: every element is read and written once (4
+// bytes).  A thread owns one slot of one token (rope.cuh), computes its eight
+// angles once and applies them to a run of heads, so the sines cost nothing
+// per head and no table goes through memory.
+#include <math.h>
+
+#include "common.cuh"
+#include "rope.cuh"
+#include "slots.cuh"
+
+namespace bsa {
+
+bsa_status launch_block_means(const bsa_kv_cache* c, int first, int count, int32_t* d_err,
+                              cudaStream_t s);
+bsa_status launch_rows_mean(const void* x_blk, float* x_mean, int B, int Hh, int D, int nb, int N,
+                            cudaStream_t s);
+
+bsa_status rope_args(const bsa_rope_desc* d, int B, int D, int T, int H, int W, RopeArgs* out,
+                     int* mode) {
+  if (d == nullptr || d->phase == nullptr) return BSA_ERR_INVALID_ARG;
+  if (d->n_axes != 1 && d->n_axes != 3) return BSA_ERR_INVALID_ARG;
+  if (d->layout != BSA_ROPE_INTERLEAVED && d->layout != BSA_ROPE_HALF) return BSA_ERR_INVALID_ARG;
+  long long P = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (d->n_pairs[i] < 0 || (d->n_axes == 1 && i > 0 && d->n_pairs[i] != 0))
+      return BSA_ERR_INVALID_ARG;
+    P += d->n_pairs[i];
+  }
+  if (P <= 0 || !isfinite(d->amplitude)) return BSA_ERR_INVALID_ARG;
+  if (P > D / 2) return BSA_ERR_SHAPE;
+  if ((reinterpret_cast<uintptr_t>(d->phase) & 7u) || (reinterpret_cast<uintptr_t>(d->pos) & 3u))
+    return BSA_ERR_INVALID_ARG;
+  RopeArgs& r = *out;
+  r.phase = reinterpret_cast<const uint64_t*>(d->phase);
+  r.pos = d->pos;
+  r.pos_stride = static_cast<long long>(B) * T * H * W;
+  r.P = static_cast<int>(P);
+  r.p0 = d->n_pairs[0];
+  r.p01 = d->n_pairs[0] + d->n_pairs[1];
+  r.n_axes = d->n_axes;
+  r.inverse = d->inverse;
+  r.H = H;
+  r.W = W;
+  r.o0 = d->origin[0];
+  r.o1 = d->origin[1];
+  r.o2 = d->origin[2];
+  r.amp = d->amplitude;
+  *mode = d->layout == BSA_ROPE_INTERLEAVED ? kRopeInterleaved
+                                            : (P % 8 == 0 ? kRopeHalf : kRopeHalfAny);
+  return BSA_OK;
+}
+
+constexpr int kRopeThreads = 256;
+constexpr int kHeadsInFlight = 4;  // heads whose vectors are loaded before any is stored
+
+// Plain 16-byte load (the tensor may be turned in place).
+__device__ __forceinline__ uint4 ld_v4(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
+  return r;
+}
+
+// Turn the slot (token `tok`, `slot`) of heads [h0, h1): row h of the source
+// is src + h * src_step, of the destination dst + h * dst_step (16-byte
+// vectors).  All of a row's slots are lanes of one warp and the warp has read
+// the rows before it writes any, so src and dst may be the same rows; `on` is
+// false for a lane without a slot.
+template <int MODE>
+__device__ __forceinline__ void turn_heads(const RopeArgs& r, const TokenPos& pos, int slot,
+                                           bool on, const uint4* src, long long src_step,
+                                           uint4* dst, long long dst_step, int h0, int h1) {
+  SlotTrig g;
+  int va, vb;
+  slot_vectors<MODE>(r.P, slot, va, vb);
+  if (MODE == kRopeHalfAny) {
+    for (int h = h0; h < h1; ++h) {
+      float a[8], b[8];
+      if (on)
+        turn_slot_any(r, pos, slot, reinterpret_cast<const __nv_bfloat16*>(src + h * src_step), a,
+                      b);
+      __syncwarp();
+      if (on) {
+        st_v4(dst + h * dst_step + va, pack8(a));
+        st_v4(dst + h * dst_step + vb, pack8(b));
+      }
+    }
+    return;
+  }
+  if (!on) return;
+  if (MODE != kRopeNone) slot_trig<MODE>(r, pos, slot, g);
+  for (int h = h0; h < h1; h += kHeadsInFlight) {
+    uint4 x[kHeadsInFlight], y[kHeadsInFlight];
+#pragma unroll
+    for (int u = 0; u < kHeadsInFlight; ++u) {
+      if (h + u < h1) {
+        x[u] = ld_v4(src + (h + u) * src_step + va);
+        y[u] = ld_v4(src + (h + u) * src_step + vb);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kHeadsInFlight; ++u) {
+      if (h + u >= h1) break;
+      if (MODE != kRopeNone) {
+        float a[8], b[8];
+        unpack8(x[u], a);
+        unpack8(y[u], b);
+        turn_slot<MODE>(g, a, b);
+        x[u] = pack8(a);
+        y[u] = pack8(b);
+      }
+      st_v4(dst + (h + u) * dst_step + va, x[u]);
+      st_v4(dst + (h + u) * dst_step + vb, y[u]);
+    }
+  }
+}
+
+struct RopeTokensArgs {
+  RopeArgs rope;
+  const uint4* x;
+  uint4* y;
+  int N, Hh, heads;  // heads per CTA
+};
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_tokens_kernel(RopeTokensArgs a) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  constexpr int kSlots = D / 16, kVecs = D / 8;
+  const int slot = threadIdx.x % kSlots;
+  const int tok = blockIdx.x * (kRopeThreads / kSlots) + threadIdx.x / kSlots;
+  const bool on = tok < a.N;
+  const long long bN = static_cast<long long>(blockIdx.z) * a.N;
+  const TokenPos pos = token_pos(a.rope, bN, on ? tok : 0);
+  const long long row = (bN + (on ? tok : 0)) * a.Hh * kVecs;
+  const int h0 = blockIdx.y * a.heads;
+  const int h1 = min(h0 + a.heads, a.Hh);
+  turn_heads<MODE>(a.rope, pos, slot, on, a.x + row, kVecs, a.y + row, kVecs, h0, h1);
+}
+
+// The chunk's tokens into blocks, K (or the one tensor) turned, V as it is:
+// one CTA per (chunk block, group of heads, batch and tensor).
+struct RopeBlocksArgs {
+  RopeArgs rope;
+  const uint4* src[2];
+  uint4* dst[2];
+  const int32_t* perm;
+  int32_t* block_valid;  // optional
+  int32_t* d_err;
+  int N, Hh, heads, tensors;
+  long long blk_stride;
+  int base_block;
+  int T, H, W;
+};
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_blocks_kernel(RopeBlocksArgs a) {
+  pdl_wait();     // global memory only after the predecessor grid completed
+  pdl_trigger();
+  constexpr int kSlots = D / 16, kVecs = D / 8;
+  __shared__ int s_tok[kBlk];
+  const int j = blockIdx.x;
+  const int b = blockIdx.z / a.tensors;
+  const int which = blockIdx.z % a.tensors;
+  const int slot0 = j * kBlk;
+  const int valid = min(kBlk, a.N - slot0);
+  const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
+  invert_block_slots<kRopeThreads>(a.perm, a.N, slot0, s_tok, j == 0 && first_cta, a.d_err, a.T,
+                                   a.H, a.W);
+  if (first_cta && a.block_valid != nullptr && threadIdx.x == 0)
+    a.block_valid[a.base_block + j] = valid;
+  // A slot of the chunk that no token maps to: perm is not a permutation.
+  if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
+  const int h0 = blockIdx.y * a.heads;
+  const int h1 = min(h0 + a.heads, a.Hh);
+  const int slot = threadIdx.x % kSlots;
+  const long long bN = static_cast<long long>(b) * a.N;
+  const long long dst_step = a.blk_stride * kBlk * kVecs;
+  for (int row = threadIdx.x / kSlots; row < kBlk; row += kRopeThreads / kSlots) {
+    const int tok = s_tok[row];
+    uint4* dst = a.dst[which] + static_cast<long long>(b) * a.Hh * dst_step +
+                 (static_cast<long long>(a.base_block + j) * kBlk + row) * kVecs;
+    if (tok < 0) {  // pad row
+      for (int h = h0; h < h1; ++h) {
+        st_v4(dst + h * dst_step + 2 * slot, make_uint4(0, 0, 0, 0));
+        st_v4(dst + h * dst_step + 2 * slot + 1, make_uint4(0, 0, 0, 0));
+      }
+    }
+    const bool on = tok >= 0;
+    const long long src_row = (bN + (on ? tok : 0)) * a.Hh * kVecs;
+    if (which == 0) {
+      const TokenPos pos = token_pos(a.rope, bN, on ? tok : 0);
+      turn_heads<MODE>(a.rope, pos, slot, on, a.src[0] + src_row, kVecs, dst, dst_step, h0, h1);
+    } else {
+      turn_heads<kRopeNone>(a.rope, TokenPos{}, slot, on, a.src[1] + src_row, kVecs, dst,
+                            dst_step, h0, h1);
+    }
+  }
+}
+
+// Heads per CTA: enough CTAs to fill the GPU, then as many heads as possible
+// for each set of angles.
+static int heads_per_cta(long long other_ctas, int Hh) {
+  const long long want = 148 * 4;
+  long long groups = (want + other_ctas - 1) / other_ctas;
+  if (groups > Hh) groups = Hh;
+  return static_cast<int>((Hh + groups - 1) / groups);
+}
+
+template <int D>
+static bsa_status launch_tokens(int mode, const RopeTokensArgs& a, int B, cudaStream_t s) {
+  constexpr int kToks = kRopeThreads / (D / 16);
+  dim3 grid((a.N + kToks - 1) / kToks, (a.Hh + a.heads - 1) / a.heads, B);
+  const dim3 block(kRopeThreads);
+  if (mode == kRopeInterleaved)
+    return launch_pdl(rope_tokens_kernel<D, kRopeInterleaved>, grid, block, 0, s, a);
+  if (mode == kRopeHalf) return launch_pdl(rope_tokens_kernel<D, kRopeHalf>, grid, block, 0, s, a);
+  return launch_pdl(rope_tokens_kernel<D, kRopeHalfAny>, grid, block, 0, s, a);
+}
+
+template <int D>
+static bsa_status launch_blocks(int mode, const RopeBlocksArgs& a, int B, int nb, cudaStream_t s) {
+  dim3 grid(nb, (a.Hh + a.heads - 1) / a.heads, B * a.tensors);
+  const dim3 block(kRopeThreads);
+  if (mode == kRopeInterleaved)
+    return launch_pdl(rope_blocks_kernel<D, kRopeInterleaved>, grid, block, 0, s, a);
+  if (mode == kRopeHalf) return launch_pdl(rope_blocks_kernel<D, kRopeHalf>, grid, block, 0, s, a);
+  return launch_pdl(rope_blocks_kernel<D, kRopeHalfAny>, grid, block, 0, s, a);
+}
+
+// Sizes every rotated call accepts.
+bsa_status check_rope_chunk(int B, int Hh, int D, int T, int H, int W) {
+  if (B <= 0 || Hh <= 0 || T <= 0 || H <= 0 || W <= 0) return BSA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
+  const long long plane = static_cast<long long>(T) * H;
+  if (plane > (1LL << 24) || plane * W > (1LL << 24)) return BSA_ERR_SHAPE;
+  if (B > 32767 || Hh > 65535) return BSA_ERR_SHAPE;
+  return BSA_OK;
+}
+
+}  // namespace bsa
+
+using namespace bsa;
+
+extern "C" bsa_status bsa_rope_frequencies(int n, double base, int scaling, double factor,
+                                           double original_length, double beta_fast,
+                                           double beta_slow, double* host_freq,
+                                           double* host_amplitude) {
+  if (host_freq == nullptr || n <= 0 || !(base > 0) || !isfinite(base)) return BSA_ERR_INVALID_ARG;
+  if (scaling < BSA_ROPE_SCALE_NONE || scaling > BSA_ROPE_SCALE_BY_PARTS)
+    return BSA_ERR_INVALID_ARG;
+  if (scaling != BSA_ROPE_SCALE_NONE && (!(factor > 0) || !isfinite(factor)))
+    return BSA_ERR_INVALID_ARG;
+  if (scaling == BSA_ROPE_SCALE_BY_PARTS &&
+      (!(original_length > 0) || !isfinite(original_length) || !(beta_fast > beta_slow) ||
+       !isfinite(beta_fast) || !isfinite(beta_slow)))
+    return BSA_ERR_INVALID_ARG;
+  const double kTwoPi = 2.0 * acos(-1.0);
+  double b = base, amp = 1.0;
+  if (scaling == BSA_ROPE_SCALE_BASE && n > 1) b *= pow(factor, static_cast<double>(n) / (n - 1));
+  if (scaling == BSA_ROPE_SCALE_BY_PARTS && factor > 1.0) amp = 0.1 * log(factor) + 1.0;
+  for (int i = 0; i < n; ++i) {
+    double f = pow(b, -static_cast<double>(i) / n);
+    if (scaling == BSA_ROPE_SCALE_LINEAR) f /= factor;
+    if (scaling == BSA_ROPE_SCALE_BY_PARTS) {
+      const double turns = original_length * f / kTwoPi;
+      double keep = (turns - beta_slow) / (beta_fast - beta_slow);
+      keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    host_freq[i] = f;
+  }
+  if (host_amplitude != nullptr) *host_amplitude = amp;
+  return BSA_OK;
+}
+
+extern "C" bsa_status bsa_rope_phases(const double* host_freq, int n, int64_t* host_phase) {
+  if (host_freq == nullptr || host_phase == nullptr || n <= 0) return BSA_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!isfinite(host_freq[i])) return BSA_ERR_INVALID_ARG;
+  const long double two_pi = 2.0L * acosl(-1.0L);
+  for (int i = 0; i < n; ++i) {
+    const long double turns = static_cast<long double>(host_freq[i]) / two_pi;
+    const long double frac = turns - floorl(turns);  // [0, 1)
+    // Rounded to 2^64 a fraction just below 1 is a whole turn: phase 0.
+    const long double scaled = roundl(ldexpl(frac, 64));
+    const uint64_t u = scaled >= 18446744073709551616.0L ? 0 : static_cast<uint64_t>(scaled);
+    host_phase[i] = static_cast<int64_t>(u);
+  }
+  return BSA_OK;
+}
+
+extern "C" bsa_status bsa_rope(const void* x_tok, void* y_tok, int B, int Hh, int D, int T, int H,
+                               int W, const bsa_rope_desc* rope, void* stream) {
+  if (x_tok == nullptr || y_tok == nullptr) return BSA_ERR_INVALID_ARG;
+  BSA_TRY(check_rope_chunk(B, Hh, D, T, H, W));
+  if (!aligned16(x_tok) || !aligned16(y_tok)) return BSA_ERR_INVALID_ARG;
+  RopeTokensArgs a{};
+  int mode;
+  BSA_TRY(rope_args(rope, B, D, T, H, W, &a.rope, &mode));
+  a.x = static_cast<const uint4*>(x_tok);
+  a.y = static_cast<uint4*>(y_tok);
+  a.N = T * H * W;
+  a.Hh = Hh;
+  const int toks = kRopeThreads / (D / 16);
+  a.heads = heads_per_cta(static_cast<long long>((a.N + toks - 1) / toks) * B, Hh);
+  return D == 128 ? launch_tokens<128>(mode, a, B, as_stream(stream))
+                  : launch_tokens<64>(mode, a, B, as_stream(stream));
+}
+
+extern "C" bsa_status bsa_tokens_to_blocks_rope(const void* x_tok, void* x_blk, float* x_mean,
+                                                int B, int Hh, int D, int T, int H, int W,
+                                                const int32_t* d_perm, const bsa_rope_desc* rope,
+                                                int32_t* d_err, void* stream) {
+  if (x_tok == nullptr || x_blk == nullptr) return BSA_ERR_INVALID_ARG;
+  BSA_TRY(check_rope_chunk(B, Hh, D, T, H, W));
+  if (!aligned16(x_tok) || !aligned16(x_blk) || !aligned16(x_mean)) return BSA_ERR_INVALID_ARG;
+  RopeBlocksArgs a{};
+  int mode;
+  BSA_TRY(rope_args(rope, B, D, T, H, W, &a.rope, &mode));
+  const int n = T * H * W;
+  if (d_perm != nullptr && n > kGatherMaxTokens) return BSA_ERR_UNSUPPORTED;
+  const int nb = (n + kBlk - 1) / kBlk;
+  a.src[0] = static_cast<const uint4*>(x_tok);
+  a.dst[0] = static_cast<uint4*>(x_blk);
+  a.perm = d_perm;
+  a.d_err = d_err;
+  a.N = n;
+  a.Hh = Hh;
+  a.tensors = 1;
+  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh);
+  a.blk_stride = nb;
+  a.T = T;
+  a.H = H;
+  a.W = W;
+  cudaStream_t s = as_stream(stream);
+  BSA_TRY(D == 128 ? launch_blocks<128>(mode, a, B, nb, s) : launch_blocks<64>(mode, a, B, nb, s));
+  return x_mean == nullptr ? BSA_OK : launch_rows_mean(x_blk, x_mean, B, Hh, D, nb, n, s);
+}
+
+extern "C" bsa_status bsa_kv_append_rope(bsa_kv_cache* c, const void* k_tok, const void* v_tok,
+                                         int T, int H, int W, const int32_t* d_perm,
+                                         const bsa_rope_desc* rope, int32_t* d_err, void* stream) {
+  if (c == nullptr || k_tok == nullptr || v_tok == nullptr || c->k == nullptr ||
+      c->v == nullptr || c->block_valid == nullptr)
+    return BSA_ERR_INVALID_ARG;
+  BSA_TRY(check_rope_chunk(c->B, c->Hh, c->D, T, H, W));
+  if (!aligned16(k_tok) || !aligned16(v_tok) || !aligned16(c->k) || !aligned16(c->v) ||
+      !aligned16(c->kmean))
+    return BSA_ERR_INVALID_ARG;
+  if (c->max_blocks <= 0 || c->n_blocks < 0 || c->n_blocks > c->max_blocks)
+    return BSA_ERR_INVALID_ARG;
+  RopeBlocksArgs a{};
+  int mode;
+  BSA_TRY(rope_args(rope, c->B, c->D, T, H, W, &a.rope, &mode));
+  const int n = T * H * W;
+  if (d_perm != nullptr && n > kGatherMaxTokens) return BSA_ERR_UNSUPPORTED;
+  const int nb = (n + kBlk - 1) / kBlk;
+  if (nb > c->max_blocks - c->n_blocks) return BSA_ERR_CAPACITY;
+  a.src[0] = static_cast<const uint4*>(k_tok);
+  a.dst[0] = static_cast<uint4*>(c->k);
+  a.src[1] = static_cast<const uint4*>(v_tok);
+  a.dst[1] = static_cast<uint4*>(c->v);
+  a.perm = d_perm;
+  a.block_valid = c->block_valid;
+  a.d_err = d_err;
+  a.N = n;
+  a.Hh = c->Hh;
+  a.tensors = 2;
+  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh);
+  a.blk_stride = c->max_blocks;
+  a.base_block = c->n_blocks;
+  a.T = T;
+  a.H = H;
+  a.W = W;
+  cudaStream_t s = as_stream(stream);
+  BSA_TRY(c->D == 128 ? launch_blocks<128>(mode, a, c->B, nb, s)
+                      : launch_blocks<64>(mode, a, c->B, nb, s));
+  if (c->kmean != nullptr) BSA_TRY(launch_block_means(c, c->n_blocks, nb, d_err, s));
+  c->n_blocks += nb;
+  return BSA_OK;
+}

@@ -1,0 +1,165 @@
+// rope.cuh - rotary positions in registers.
+//
+// A row of D elements is handled in D/16 slots; a thread owns one slot of a
+// row: two 16-byte vectors that hold eight whole pairs (or none), so a pair
+// never crosses threads and a row may be turned in place.
+//   interleaved   slot s: vectors 2s and 2s + 1, pairs 8s .. 8s + 7
+//   half, P % 8 = 0  slot s < P/8: vectors s and s + P/8, pairs 8s .. 8s + 7;
+//                 the vectors past 2P, two a slot, are copied
+//   half, any P   the elements of pair i and i + P fall anywhere in their
+//                 vectors: slot s owns elements 16s .. 16s + 15 of the output
+//                 and fetches each element's partner by itself (kHalfAny)
+// The angle is exact: phase[i] is the pair's frequency as a 64-bit fraction
+// of a turn, p * phase mod 2^64 the fraction turned, whose top 32 bits (an
+// error below 2^-32 turn) go to sincospif as half turns in [-1, 1).
+#pragma once
+
+#include "common.cuh"
+
+namespace bsa {
+
+enum RopeMode { kRopeNone = 0, kRopeInterleaved = 1, kRopeHalf = 2, kRopeHalfAny = 3 };
+
+struct RopeArgs {
+  const uint64_t* phase;
+  const int32_t* pos;   // [n_axes, B, N] or null
+  long long pos_stride; // B * N
+  int P, p0, p01;       // pairs in all, of axis 0, of axes 0 and 1
+  int n_axes, inverse;
+  int H, W;
+  int o0, o1, o2;       // origin
+  float amp;
+};
+
+struct TokenPos {
+  int p[3];
+};
+
+// Positions of raster token `tok` of batch b; bN = b * N.
+__device__ __forceinline__ TokenPos token_pos(const RopeArgs& r, long long bN, int tok) {
+  TokenPos t;
+  if (r.pos != nullptr) {
+    const int32_t* q = r.pos + bN + tok;
+    t.p[0] = __ldg(q);
+    t.p[1] = r.n_axes == 3 ? __ldg(q + r.pos_stride) : 0;
+    t.p[2] = r.n_axes == 3 ? __ldg(q + 2 * r.pos_stride) : 0;
+  } else if (r.n_axes == 3) {
+    const int row = tok / r.W;
+    t.p[2] = tok - row * r.W;
+    t.p[0] = row / r.H;
+    t.p[1] = row - t.p[0] * r.H;
+  } else {
+    t.p[0] = tok;
+    t.p[1] = t.p[2] = 0;
+  }
+  return t;
+}
+
+// cos and sin of pair i (amplitude and direction applied).
+__device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, int i, float& c,
+                                          float& s) {
+  const int ax = i < r.p0 ? 0 : (i < r.p01 ? 1 : 2);
+  const long long p = static_cast<long long>(ax == 0 ? t.p[0] : (ax == 1 ? t.p[1] : t.p[2])) +
+                      (ax == 0 ? r.o0 : (ax == 1 ? r.o1 : r.o2));
+  const uint64_t turn = static_cast<uint64_t>(p) * __ldg(r.phase + i);
+  const int32_t hi = static_cast<int32_t>(turn >> 32);
+  sincospif(static_cast<float>(hi) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  c *= r.amp;
+  s *= r.inverse ? -r.amp : r.amp;
+}
+
+// The eight pairs of a slot; pairs at or past P are left alone.
+struct SlotTrig {
+  float c[8], s[8];
+  int n;  // pairs of the slot that are turned, 0..8
+};
+
+template <int MODE>
+__device__ __forceinline__ void slot_trig(const RopeArgs& r, const TokenPos& t, int slot,
+                                          SlotTrig& g) {
+  const int n = r.P - slot * 8;
+  g.n = n < 0 ? 0 : (n > 8 ? 8 : n);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    g.c[e] = 1.f;
+    g.s[e] = 0.f;
+    if (e < g.n) pair_trig(r, t, slot * 8 + e, g.c[e], g.s[e]);
+  }
+}
+
+// The two vectors of a slot.
+template <int MODE>
+__device__ __forceinline__ void slot_vectors(int P, int slot, int& va, int& vb) {
+  if (MODE == kRopeHalf && slot < P / 8) {
+    va = slot;
+    vb = slot + P / 8;
+  } else {
+    // Half layout: P/8 slots have taken the first P/4 vectors, so the
+    // copied ones are again two a slot, at 2s and 2s + 1.
+    va = 2 * slot;
+    vb = 2 * slot + 1;
+  }
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  x[0] = bf16lo(v.x); x[1] = bf16hi(v.x); x[2] = bf16lo(v.y); x[3] = bf16hi(v.y);
+  x[4] = bf16lo(v.z); x[5] = bf16hi(v.z); x[6] = bf16lo(v.w); x[7] = bf16hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+__device__ __forceinline__ void turn_pair(float& x, float& y, float c, float s) {
+  const float a = x * c - y * s;
+  y = x * s + y * c;
+  x = a;
+}
+
+// Turn a slot's sixteen values a (vector va) and b (vector vb).
+template <int MODE>
+__device__ __forceinline__ void turn_slot(const SlotTrig& g, float (&a)[8], float (&b)[8]) {
+  if (MODE == kRopeInterleaved) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (e < g.n) turn_pair(a[2 * e], a[2 * e + 1], g.c[e], g.s[e]);
+      if (e + 4 < g.n) turn_pair(b[2 * e], b[2 * e + 1], g.c[e + 4], g.s[e + 4]);
+    }
+  } else if (MODE == kRopeHalf) {
+    if (g.n != 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) turn_pair(a[e], b[e], g.c[e], g.s[e]);
+    }
+  }
+}
+
+// kHalfAny: the output elements 16*slot .. 16*slot + 15 of `row`.
+__device__ __forceinline__ void turn_slot_any(const RopeArgs& r, const TokenPos& t, int slot,
+                                              const __nv_bfloat16* row, float (&a)[8],
+                                              float (&b)[8]) {
+#pragma unroll 1
+  for (int e = 0; e < 16; ++e) {
+    const int el = slot * 16 + e;
+    float v = __bfloat162float(row[el]);
+    if (el < 2 * r.P) {
+      const bool second = el >= r.P;
+      const int i = second ? el - r.P : el;
+      const float w = __bfloat162float(row[second ? i : i + r.P]);
+      float c, s;
+      pair_trig(r, t, i, c, s);
+      v = second ? w * s + v * c : v * c - w * s;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // registers: no indexed store
+      if (e == k) a[k] = v;
+      if (e == k + 8) b[k] = v;
+    }
+  }
+}
+
+// Checks a descriptor and fills the kernel's arguments; `mode` is how the
+// kernels handle its layout.
+bsa_status rope_args(const bsa_rope_desc* d, int B, int D, int T, int H, int W, RopeArgs* out,
+                     int* mode);
+
+}  // namespace bsa

@@ -1144,7 +1144,8 @@ static bsa_status route_scores(const void* q_blk, const float* q_mean, const bsa
                                int32_t* idx, int32_t* cnt, int max_sel, void* workspace,
                                size_t ws_bytes, int32_t* d_err, cudaStream_t s, RouteArgs* out) {
   if ((q_blk == nullptr && q_mean == nullptr) || c == nullptr || idx == nullptr ||
-      cnt == nullptr || workspace == nullptr || c->k == nullptr || c->block_valid == nullptr)
+      cnt == nullptr || workspace == nullptr || c->block_valid == nullptr ||
+      (c->k == nullptr && c->kmean == nullptr))  // pooled keys: the cache's keys are not read
     return BSA_ERR_INVALID_ARG;
   if (q_mean != nullptr && !aligned16(q_mean)) return BSA_ERR_INVALID_ARG;
   if (q_mean != nullptr) q_blk = c->k;  // not read; keeps the alignment check below uniform

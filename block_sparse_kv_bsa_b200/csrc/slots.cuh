@@ -1,0 +1,94 @@
+// slots.cuh - which raster token sits in each slot of a 128-token block.
+//
+// Shared by the kernels that gather a chunk's tokens into blocks (append,
+// query reordering, their rotated and 8-bit forms).
+#pragma once
+
+#include "common.cuh"
+#include "gilbert.cuh"
+
+namespace bsa {
+
+// Chunks up to this size invert a permutation table per block (a scan).
+constexpr int kGatherMaxTokens = 1 << 14;
+
+// The curve walk kept out of line: the kernels' table path stays compact.
+static __device__ __noinline__ int curve_token_call(int T, int H, int W, int p) {
+  return curve_token(T, H, W, p);
+}
+
+// Slot -> token for the 128 curve slots [slot0, slot0 + 128) of one block:
+// s_tok[d] is the raster token whose perm entry is slot0 + d, or -1.  The
+// CTA's NT threads (NT >= 128) scan perm in rounds of kScan independent loads
+// per thread (one L2 round trip per round); entries outside [0, N) are
+// skipped, and reported when `report_bad`.  Ends with a CTA barrier.
+// s_tok[d] = the token at curve slot slot0 + d (d < 128), or -1 for a pad
+// slot.  With a table, the CTA scans perm (token -> slot); without one
+// (perm == NULL), each thread locates its slot on the curve.
+template <int NT>
+__device__ __forceinline__ void invert_block_slots(const int32_t* perm, int N, int slot0,
+                                                   int* s_tok, bool report_bad, int32_t* d_err,
+                                                   int T, int H, int W) {
+  static_assert(NT >= kBlk, "one thread per slot clears the table");
+  if (perm == nullptr) {
+    if (threadIdx.x < kBlk) {
+      const int p = slot0 + static_cast<int>(threadIdx.x);
+      s_tok[threadIdx.x] = p < N ? curve_token_call(T, H, W, p) : -1;
+    }
+    __syncthreads();
+    return;
+  }
+  if (threadIdx.x < kBlk) s_tok[threadIdx.x] = -1;
+  __syncthreads();
+  auto take = [&](int r, int p) {
+    if (p < 0 || p >= N) {
+      if (report_bad) report(d_err, BSA_DEV_BAD_PERM);
+      return;
+    }
+    const unsigned d = static_cast<unsigned>(p - slot0);
+    if (d < static_cast<unsigned>(kBlk)) s_tok[d] = r;
+  };
+  constexpr int kScan = 16;
+  // Four entries per load when perm is 16-byte aligned: one round of loads
+  // covers 64 * NT tokens, so a chunk's scan costs one memory latency.
+  int done = 0;
+  if ((reinterpret_cast<uintptr_t>(perm) & 15u) == 0) {
+    const int n4 = N / 4;
+    const int4* perm4 = reinterpret_cast<const int4*>(perm);
+    for (int base = 0; base < n4; base += kScan * NT) {
+      int4 pv[kScan];
+#pragma unroll
+      for (int k = 0; k < kScan; ++k) {
+        const int i = base + threadIdx.x + k * NT;
+        pv[k] = i < n4 ? __ldg(perm4 + i) : make_int4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < kScan; ++k) {
+        const int i = base + threadIdx.x + k * NT;
+        if (i >= n4) break;
+        take(4 * i, pv[k].x);
+        take(4 * i + 1, pv[k].y);
+        take(4 * i + 2, pv[k].z);
+        take(4 * i + 3, pv[k].w);
+      }
+    }
+    done = 4 * n4;
+  }
+  for (int base = done; base < N; base += kScan * NT) {
+    int pv[kScan];
+#pragma unroll
+    for (int k = 0; k < kScan; ++k) {
+      const int r = base + threadIdx.x + k * NT;
+      pv[k] = r < N ? __ldg(perm + r) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kScan; ++k) {
+      const int r = base + threadIdx.x + k * NT;
+      if (r >= N) break;
+      take(r, pv[k]);
+    }
+  }
+  __syncthreads();
+}
+
+}  // namespace bsa

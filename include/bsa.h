@@ -23,6 +23,7 @@
  *   Streams    `stream` is a cudaStream_t passed as void* (NULL = the legacy
  *              default stream).  All device work is asynchronous on it.
  *   Types      Q, K, V and O are bf16; g and LSE are fp32; indices int32.
+ *              The 8-bit cache (bsa_kv_cache8) holds K and V in e4m3.
  *   Layout     Dense, row-major, no strides:
  *                token layout  [B, T*H*W, Hh, D]   raster (t, h, w) order
  *                block layout  [B, Hh, n_blocks, 128, D]
@@ -71,6 +72,7 @@ typedef enum bsa_status {
 #define BSA_DEV_BAD_VALID 3    /* a block_valid entry outside [1, 128] */
 #define BSA_DEV_BAD_PERM 4     /* a permutation entry outside the chunk */
 #define BSA_DEV_WAIT_TIMEOUT 5 /* a bounded pipeline wait gave up */
+#define BSA_DEV_BAD_SCALE 6    /* an 8-bit block scale that is not finite and > 0 */
 
 /*
  * Caller-owned view of the block KV cache.
@@ -199,7 +201,9 @@ bsa_status bsa_route_workspace_size(int B, int Hh, int D, int n_q_blocks, int n_
  * Arithmetic is fp32 with a fixed reduction order; with the pooled-key
  * cache and at most 64 query blocks, <qm, km> runs on the tensor core as
  * three tf32 products of hi/lo splits of both means (about fp32's
- * precision, fixed order), so results are deterministic either way.
+ * precision, fixed order), so results are deterministic either way.  With
+ * the pooled-key cache the keys themselves are not read and cache->k may be
+ * NULL.
  *   q_blk      device bf16 [B, Hh, n_own*128, D] (block order)
  *   q_valid    device int32 [n_own] valid rows per query block, or NULL to
  *              use cache->block_valid[own_first + j]
@@ -426,6 +430,199 @@ bsa_status bsa_route_noalloc(const void *q_blk, const bsa_kv_cache *cache, const
                              float lambda, float g_ref, float sm_scale, int top_k,
                              int32_t *idx, int32_t *cnt, int max_sel, int32_t *d_err,
                              void *stream);
+
+/*
+ * Rotary positions.
+ *
+ * A pair (x, y) of a head's elements is turned by the angle theta = p * f,
+ * f radians per unit of position, p the token's position on the pair's axis:
+ *   (x, y) -> amplitude * (x cos theta - y sin theta, x sin theta + y cos theta).
+ * P = n_pairs[0] + n_pairs[1] + n_pairs[2] <= D / 2 pairs are turned, the
+ * first n_pairs[0] by the t position, the next n_pairs[1] by h, the rest by
+ * w; the elements past 2 P pass unchanged.  Pair i is elements (2i, 2i + 1)
+ * (BSA_ROPE_INTERLEAVED) or (i, i + P) (BSA_ROPE_HALF).
+ *   phase      device int64 [P] (8-byte aligned): f as a 64-bit fraction of
+ *              a turn, round(f / (2 pi) * 2^64) mod 2^64 (bsa_rope_phases).
+ *              p * phase mod 2^64 is then the exact fraction of a turn, so
+ *              angles of far positions lose nothing.
+ *   n_axes     3: positions (t, h, w); 1: one position, n_pairs[1] =
+ *              n_pairs[2] = 0
+ *   pos        device int32 [n_axes, B, T*H*W]: the position of every raster
+ *              token, or NULL for those of the grid: origin[0] + t,
+ *              origin[1] + h, origin[2] + w (n_axes = 1: origin[0] + the
+ *              raster index)
+ *   origin     added to every position, also those of pos
+ *   inverse    nonzero: turn by -theta.  With the same amplitude this is the
+ *              transposed map: applied to the gradient of the turned
+ *              tensor it gives the gradient of the tensor.
+ * Arithmetic is fp32, rounded once to the output type.
+ */
+#define BSA_ROPE_INTERLEAVED 0
+#define BSA_ROPE_HALF 1
+typedef struct bsa_rope_desc {
+  const int64_t *phase;
+  int32_t n_pairs[3];
+  int32_t n_axes;
+  int32_t layout;
+  int32_t inverse;
+  float amplitude;
+  const int32_t *pos;
+  int32_t origin[3];
+} bsa_rope_desc;
+
+/*
+ * Frequencies of n_pairs pairs (host only, fp64): f[i] = base^(-i / n_pairs)
+ * radians per position, changed for longer contexts by `scaling`:
+ *   BSA_ROPE_SCALE_NONE      as they are (factor and the rest unused)
+ *   BSA_ROPE_SCALE_LINEAR    f / factor (positions interpolated)
+ *   BSA_ROPE_SCALE_BASE      base * factor^(n / (n - 1)) instead of base: the
+ *                            first pair keeps its frequency, the last is
+ *                            divided by factor (n = 1: unchanged)
+ *   BSA_ROPE_SCALE_BY_PARTS  pairs that make at least beta_fast turns over
+ *                            original_length positions keep f, those with
+ *                            at most beta_slow turns get f / factor, with a
+ *                            linear ramp over the turns in between;
+ *                            amplitude 0.1 ln(factor) + 1 (1 for factor <= 1)
+ *   host_freq       host double [n_pairs], written
+ *   host_amplitude  host double, written (1 but for BY_PARTS), or NULL
+ * Errors: BSA_ERR_INVALID_ARG (null, n_pairs <= 0, base, factor or
+ *         original_length not positive and finite, beta_fast <= beta_slow).
+ */
+#define BSA_ROPE_SCALE_NONE 0
+#define BSA_ROPE_SCALE_LINEAR 1
+#define BSA_ROPE_SCALE_BASE 2
+#define BSA_ROPE_SCALE_BY_PARTS 3
+bsa_status bsa_rope_frequencies(int n_pairs, double base, int scaling, double factor,
+                                double original_length, double beta_fast, double beta_slow,
+                                double *host_freq, double *host_amplitude);
+
+/*
+ * The phase table of host frequencies (radians per position, fp64; host
+ * only): host_phase[i] = round(frac(host_freq[i] / (2 pi)) * 2^64).
+ * Errors: BSA_ERR_INVALID_ARG (null, n <= 0, a frequency that is not finite).
+ */
+bsa_status bsa_rope_phases(const double *host_freq, int n, int64_t *host_phase);
+
+/*
+ * Rotary positions of a chunk (or, with H = W = 1, of T tokens of a
+ * sequence) in raster token order, or with rope->inverse the gradient:
+ *   x_tok  device bf16 [B, T*H*W, Hh, D]
+ *   y_tok  device bf16, the same shape; may be x_tok (in place), and must not
+ *          overlap it otherwise
+ * Errors: BSA_ERR_INVALID_ARG, BSA_ERR_SHAPE (B or Hh above 65535, T*H*W
+ *         above 2^24), BSA_ERR_UNSUPPORTED (D), BSA_ERR_CUDA.
+ */
+bsa_status bsa_rope(const void *x_tok, void *y_tok, int B, int Hh, int D, int T, int H, int W,
+                    const bsa_rope_desc *rope, void *stream);
+
+/*
+ * bsa_tokens_to_blocks (or, with x_mean, bsa_tokens_to_blocks_mean) of the
+ * turned tokens, in one pass: x_blk holds the turned values rounded to bf16,
+ * x_mean (device fp32 [B, Hh, nb, D], 16-byte aligned, or NULL) the means of
+ * the rounded rows, in the library's fixed order.  With a table (d_perm),
+ * chunks of up to 16384 tokens; without one, up to 2^24.
+ * Errors: those of bsa_rope and bsa_tokens_to_blocks; BSA_ERR_UNSUPPORTED
+ *         above 16384 tokens with a table.
+ */
+bsa_status bsa_tokens_to_blocks_rope(const void *x_tok, void *x_blk, float *x_mean, int B, int Hh,
+                                     int D, int T, int H, int W, const int32_t *d_perm,
+                                     const bsa_rope_desc *rope, int32_t *d_err, void *stream);
+
+/*
+ * bsa_kv_append with the keys turned on the way into the cache (V is moved
+ * as it is).  cache->kmean, when present, gets the means of the turned keys
+ * as stored.  Chunk sizes as for bsa_tokens_to_blocks_rope.
+ * Errors: those of bsa_kv_append and bsa_tokens_to_blocks_rope.
+ */
+bsa_status bsa_kv_append_rope(bsa_kv_cache *cache, const void *k_tok, const void *v_tok, int T,
+                              int H, int W, const int32_t *d_perm, const bsa_rope_desc *rope,
+                              int32_t *d_err, void *stream);
+
+/*
+ * A block KV cache held in 8 bits: e4m3 codes with one fp32 scale per block
+ * of 128 tokens and head.  A key is code * k_scale, a value code * v_scale.
+ *   k, v              device e4m3 [B, Hh, max_blocks, 128, D], 16-byte aligned
+ *   k_scale, v_scale  device fp32 [B, Hh, max_blocks]: finite and > 0 for
+ *                     every block in use (else BSA_DEV_BAD_SCALE, and the
+ *                     block's scale counts as 1)
+ * The rest is bsa_kv_cache's.  kmean, when present, makes the router work on
+ * this cache: the route calls take a bsa_kv_cache with k = v = NULL and this
+ * cache's block_valid, kmean and sizes.
+ */
+typedef struct bsa_kv_cache8 {
+  void *k;
+  void *v;
+  float *k_scale;
+  float *v_scale;
+  int32_t *block_valid;
+  int32_t B, Hh, D;
+  int32_t max_blocks;
+  int32_t n_blocks;
+  float *kmean;
+} bsa_kv_cache8;
+
+/*
+ * bsa_kv_append into an 8-bit cache, the keys turned on the way when rope is
+ * given (NULL: not turned).  For every (batch, head, new block) and each of
+ * K (turned, in fp32, not rounded in between) and V, over the block's valid
+ * rows r:
+ *   A     = max(largest finite |r|, 2^-64),  scale = A / 448,
+ *   code  = e4m3(r * (448 / A)), round to nearest even; infinities become
+ *           +-448 and NaN stays NaN.
+ * Pad rows get code 0.  cache->kmean, when present, gets the fp32 mean of the
+ * block's valid turned key rows before they are rounded to 8 bits.  Chunk
+ * sizes as for bsa_tokens_to_blocks_rope.
+ * Errors: those of bsa_kv_append_rope.
+ */
+bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v_tok, int T,
+                          int H, int W, const int32_t *d_perm, const bsa_rope_desc *rope,
+                          int32_t *d_err, void *stream);
+
+/*
+ * bsa_attn over an 8-bit cache, with grouped heads: Hq query heads, a
+ * multiple of the cache's Hh; query head h reads cache head h / (Hq / Hh) and
+ * that head's route.  Products are f16 on the tensor core (e4m3 codes and
+ * bf16 queries, scaled per row by a power of two, are exact in f16 but for
+ * query elements below 2^-29 of the row's largest), accumulated in fp32; the
+ * softmax weights are rounded to f16.
+ *   q_blk    device bf16 [B, Hq, n_q_blocks*128, D]
+ *   idx,cnt  device int32 [B, Hh, n_q_blocks, max_sel], [B, Hh, n_q_blocks]
+ *   o_blk    device bf16, q_blk's shape;  lse device fp32 [B, Hq, n_q_blocks*128]
+ * Everything else is bsa_attn's.  Rows of a block past its valid count are
+ * never read as values: what they hold (NaN included) does not matter.
+ * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh;
+ *         on the device also BSA_DEV_BAD_SCALE.
+ */
+bsa_status bsa_kv8_attn(const void *q_blk, const bsa_kv_cache8 *cache, int Hq,
+                        const int32_t *q_valid, const int32_t *idx, const int32_t *cnt,
+                        int n_q_blocks, int max_sel, float sm_scale, void *o_blk, float *lse,
+                        int32_t *d_err, void *stream);
+
+/* Device workspace bsa_kv8_attn_decode needs, in bytes, for n_sel blocks
+ * (max_sel of a route, or the cache's n_blocks without one); it suffices for
+ * any smaller n_sel. */
+bsa_status bsa_kv8_attn_decode_workspace_size(int B, int Hq, int Hh, int D, int n_tok, int n_sel,
+                                              size_t *bytes);
+
+/*
+ * The form for single tokens: n_tok query tokens (1 upward, n_tok * Hq / Hh
+ * at most 128) of every batch entry attend over the blocks of one route per
+ * cache head, or over the whole cache.  The keys are split over the GPU and
+ * the parts joined by a second kernel, in a fixed order.
+ *   q_tok    device bf16 [B, n_tok, Hq, D]
+ *   idx,cnt  device int32 [B, Hh, max_sel], [B, Hh], or both NULL: every
+ *            block in use, [0, n_blocks) (max_sel is then not read)
+ *   o_tok    device bf16 [B, n_tok, Hq, D];  lse device fp32 [B, n_tok, Hq]
+ * A query with an empty route gets O = 0 and LSE = -inf.
+ *   workspace  device, at least bsa_kv8_attn_decode_workspace_size bytes,
+ *              256-aligned; calls that may overlap need one each
+ * Errors: those of bsa_kv8_attn; BSA_ERR_CAPACITY (workspace too small);
+ *         BSA_ERR_UNSUPPORTED (more than 128 query rows per cache head).
+ */
+bsa_status bsa_kv8_attn_decode(const void *q_tok, const bsa_kv_cache8 *cache, int Hq, int n_tok,
+                               const int32_t *idx, const int32_t *cnt, int max_sel,
+                               float sm_scale, void *o_tok, float *lse, void *workspace,
+                               size_t ws_bytes, int32_t *d_err, void *stream);
 
 /*
  * Synchronise `stream`, read d_err, clear it, and map it to a status:
