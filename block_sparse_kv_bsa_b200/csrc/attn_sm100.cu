@@ -54,13 +54,11 @@
 // in-flight copies and MMAs finish (bounded) and frees tensor memory.  Every
 // warp runs the same sequence of named-barrier operations whether or not a
 // wait gave up, so an abort never leaves a partner waiting at a barrier.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
 #include "common.cuh"
 #include "gilbert.cuh"
+#include "tma_host.cuh"
 
 namespace bsa {
 
@@ -669,7 +667,7 @@ bsa_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 // ---------------------------------------------------------------------------
 // Host side: tensor maps and launch
 // ---------------------------------------------------------------------------
-static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {

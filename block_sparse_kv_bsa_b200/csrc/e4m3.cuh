@@ -16,6 +16,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t pack_e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // The two codes of the low (high) half of w to f16 pairs, exactly.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
   uint32_t r;

@@ -10,10 +10,11 @@
 // in the same order.
 #include "common.cuh"
 #include "attn8_warp.cuh"
+#include "tma_host.cuh"
 
 namespace bsa {
 
-bool device_is_sm100();
+
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = kDecWarps * 32;

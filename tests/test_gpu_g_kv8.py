@@ -279,6 +279,22 @@ def test_attn8_order_of_the_route_and_repeats():
     assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
 
 
+def test_attn8_gives_the_same_bits_every_time():
+    # 640 query blocks over several waves of CTAs, 60 times: a tile read
+    # before it is whole, or overwritten while it is read, shows as a changed bit.
+    B, Hh, D, nqb, blocks, n = 1, 16, 128, 40, 200, 25
+    cache = ref.fill_cache(bsa, B, Hh, D, blocks, [128] * 199 + [31], 55)
+    g = torch.Generator(device=DEV).manual_seed(56)
+    q = (torch.randn((B, Hh, nqb * 128, D), generator=g, device=DEV) * 3).to(torch.bfloat16)
+    idx, cnt = random_route(B, Hh, nqb, blocks, [n], n, 57)
+    want = None
+    for _ in range(60):
+        got = bsa.bsa_kv8_attn(q, cache, idx, cnt)
+        if want is None:
+            want = got
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("what,code", [("index", 1), ("count", 2), ("valid", 3), ("scale", 6),
                                        ("nan", 6)])
 def test_attn8_reports_what_only_the_device_sees(what, code):
