@@ -115,14 +115,26 @@ __device__ __forceinline__ void bar_sync8(int id, int count) {
 __device__ __forceinline__ void bar_arrive8(int id, int count) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
-// A load the compiler keeps in its place among the barrier operations.
-__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
-  uint4 r;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr)
-               : "memory");
+// Shared-memory accesses by 32-bit address (the aligned base pointer is a
+// generic one to the compiler), kept in their place among the barrier
+// operations.
+__device__ __forceinline__ uint2 lds_v2(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
   return r;
+}
+__device__ __forceinline__ void sts_v4(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ float lds_f(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ void sts_f(uint32_t addr, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float d;
@@ -179,7 +191,7 @@ __device__ __forceinline__ int clamp_block(const Attn8Args& a, int blk) {
 // memory; returns the row's scale.  All 256 softmax threads take part.
 template <int D>
 __device__ __forceinline__ float split_query(const Attn8Args& a, long long item, int g, int r,
-                                             uint8_t* q_terms, float* tok) {
+                                             uint8_t* q_terms, uint32_t tok) {
   const __nv_bfloat16* src = a.q + (item * kBlk + r) * D + g * (D / 2);
   uint4 raw[D / 16];
   float amax = 0.f;
@@ -194,9 +206,9 @@ __device__ __forceinline__ float split_query(const Attn8Args& a, long long item,
       amax = max3(amax, x <= 3.402823466e38f ? x : 0.f, y <= 3.402823466e38f ? y : 0.f);
     }
   }
-  tok[g * kBlk + r] = amax;
+  sts_f(tok + (g * kBlk + r) * 4, amax);
   bar_sync8(9, kSoftmax8);
-  amax = fmaxf(tok[r], tok[kBlk + r]);
+  amax = fmaxf(lds_f(tok + r * 4), lds_f(tok + (kBlk + r) * 4));
   bar_sync8(9, kSoftmax8);  // tok is the softmax's from here on
   // Largest magnitude to [2^7, 2^8); a zero row is not scaled.
   int e = (__float_as_int(amax) >> 23) - 127 - 7;
@@ -402,17 +414,20 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     }
   } else if (warp >= 12) {
     // ---------------- V tiles to f16 ----------------
-    // Thread i takes 16-byte chunk i, i + 128, ... of the staged tile (16
-    // values of a row) and writes two f16 chunks of the swizzled tile the P V
-    // reads (64-column boxes of 128 rows x 128 bytes, chunk c of row r at c ^
-    // (r % 8)).  The upper half of a row's lanes writes its odd chunk first, so
-    // that eight lanes always write eight different chunk positions.
+    // A thread turns 8 codes into one 16-byte chunk of f16 per step: chunk c of
+    // row r goes to position c ^ (r % 8) of its 64-column box (128 rows x 128
+    // bytes), the swizzled tile the P V reads.  Eight lanes write eight
+    // different positions, and a thread's steps are whole multiples of 8
+    // rows apart, so its addresses differ by a constant.
     regs_dec<kRegsConvert>();
     const int i0 = threadIdx.x - 384;
-    constexpr int kPer = L::kTile8 / 16 / kConvert8;  // chunks per thread
-    constexpr int kRowChunks = D / 16;
-    const int c = i0 % kRowChunks;
-    const int swap = D == 128 ? (c >> 2) & 1 : 0;
+    constexpr int kRowChunks = D / 8;
+    constexpr int kRowStep = kConvert8 / kRowChunks;
+    constexpr int kPer = kBlk / kRowStep;  // chunks per thread
+    const int c = i0 & (kRowChunks - 1), r0 = i0 / kRowChunks;
+    const uint32_t src0 = smem_u32(sm + L::kV8) + i0 * 8;
+    const uint32_t dst0 = smem_u32(sm + L::kV16) + (c >> 3) * (kBlk * 128) + r0 * 128 +
+                          (((c & 7) ^ (r0 & 7)) << 4);
     bool ok = true;
     int blk = n > 0 ? route[0] : 0;
     for (int t = 0; ok && t < n; ++t) {
@@ -425,30 +440,27 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_V8_FULL + s8], (t / kV8Slots) & 1,
                                                      s_abort, kWait8));
       if (!ok) break;
-      const uint32_t src = smem_u32(sm + L::kV8 + s8 * L::kTile8) + i0 * 16;
-      uint4 x[kPer];
+      const uint32_t src = src0 + s8 * L::kTile8;
+      uint2 x[kPer];
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) x[u] = lds_v4(src + u * (kConvert8 * 16));
+      for (int u = 0; u < kPer; ++u) x[u] = lds_v2(src + u * (kConvert8 * 8));
       mbar_arrive(&bars[A_V8_EMPTY + s8]);
       if (t >= kV16Slots) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_V_EMPTY + sl],
                                                        ((t / kV16Slots) - 1) & 1, s_abort, kWait8));
         if (!ok) break;
       }
-      uint8_t* dst = sm + L::kV16 + sl * L::kTile16;
+      if (valid < kBlk) {
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int r = (i0 + u * kConvert8) / kRowChunks;
-        if (r >= valid) x[u] = make_uint4(0, 0, 0, 0);
-        const uint4 lo = make_uint4(e4m3_lo_f16x2(x[u].x), e4m3_hi_f16x2(x[u].x),
-                                    e4m3_lo_f16x2(x[u].y), e4m3_hi_f16x2(x[u].y));
-        const uint4 hi = make_uint4(e4m3_lo_f16x2(x[u].z), e4m3_hi_f16x2(x[u].z),
-                                    e4m3_lo_f16x2(x[u].w), e4m3_hi_f16x2(x[u].w));
-        uint8_t* row = dst + (c >> 2) * (kBlk * 128) + r * 128;
-        const int p0 = ((2 * c) & 7) ^ (r & 7), p1 = ((2 * c + 1) & 7) ^ (r & 7);
-        *reinterpret_cast<uint4*>(row + (swap ? p1 : p0) * 16) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (swap ? p0 : p1) * 16) = swap ? lo : hi;
+        for (int u = 0; u < kPer; ++u)
+          if (r0 + u * kRowStep >= valid) x[u] = make_uint2(0, 0);
       }
+      const uint32_t dst = dst0 + sl * L::kTile16;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+        sts_v4(dst + u * (kRowStep * 128),
+               make_uint4(e4m3_lo_f16x2(x[u].x), e4m3_hi_f16x2(x[u].x), e4m3_lo_f16x2(x[u].y),
+                          e4m3_hi_f16x2(x[u].y)));
       fence_proxy_async_smem();
       mbar_arrive(&bars[A_PV_READY + sl]);
     }
@@ -465,7 +477,8 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     const int wq = warp & 3;                 // TMEM lane window of this warp
     const int r = wq * 32 + lane;            // query row owned by this thread
     const uint32_t lane_base = static_cast<uint32_t>(wq * 32) << 16;
-    float* tok = reinterpret_cast<float*>(sm + L::kTok);  // [2 warpgroups][128 rows]
+    const uint32_t tok = smem_u32(sm + L::kTok);  // float [2 warpgroups][128 rows]
+    const uint32_t tok_mine = tok + (g * kBlk + r) * 4, tok_other = tok + ((g ^ 1) * kBlk + r) * 4;
     const int bar_in = 1 + (g ^ 1) * 4 + wq;
     const int bar_out = 1 + g * 4 + wq;
 
@@ -538,11 +551,11 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       float m_prev = -INFINITY;
       if (t > 0) {
         bar_sync8(bar_in, 64);
-        m_prev = tok[(g ^ 1) * kBlk + r];
+        m_prev = lds_f(tok_other);
       }
       const float m_t = (t == 0 || mx > m_prev + kMoveAt) ? mx - kBias : m_prev;
       if (t + 1 < n) {
-        tok[g * kBlk + r] = m_t;
+        sts_f(tok_mine, m_t);
         bar_arrive8(bar_out, 64);
       }
 
