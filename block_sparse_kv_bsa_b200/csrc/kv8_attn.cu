@@ -29,6 +29,9 @@
 //               staging slots, plain bulk copies), V two tiles behind K
 //   warp 1      tensor memory; issues O += P_t V_t
 //   warp 2      issues S_t = Q K_t^T
+//   warp 3      each tile's scales and valid count, 32 tiles at a time, checked
+//               and as the other warps use them (read from global memory by
+//               every softmax thread they cost 4 % of the call)
 //   warps 4-11  softmax: two warpgroups, alternate tiles, a thread per row;
 //               before that they split Q into its two 8-bit terms
 //   warps 12-15 V tiles from e4m3 to f16 (rows past a block's valid count
@@ -60,6 +63,8 @@ constexpr float kMoveAt = 15.f;    // a weight past 2^15 moves the reference
 // the block is launched with.
 constexpr int kRegsIssue = 64, kRegsSoftmax = 176, kRegsConvert = 96;
 
+constexpr int kMetaTiles = 32;  // tiles of a half of the metadata ring
+
 enum {
   A_Q_FULL = 0,                         // Q terms written (256 threads)
   A_K_FULL = 1,                         // + K slot
@@ -69,7 +74,9 @@ enum {
   A_V_EMPTY = A_V8_EMPTY + kV8Slots,    // + V slot: its P V is done
   A_PV_READY = A_V_EMPTY + kV16Slots,   // + slot t % 3: P_t stored and V_t converted
   A_S_FULL = A_PV_READY + kV16Slots,    // + S buffer
-  A_MMA_DONE = A_S_FULL + kS8Bufs,      // + issuer
+  A_META_FULL = A_S_FULL + kS8Bufs,     // + half of the ring: 32 tiles' scales (32 threads)
+  A_META_EMPTY = A_META_FULL + 2,       // + half: read by all 384 threads
+  A_MMA_DONE = A_META_EMPTY + 2,        // + issuer
   A_COUNT = A_MMA_DONE + 2
 };
 
@@ -84,7 +91,8 @@ struct Layout8 {
   static constexpr int kBars = kV8 + kV8Slots * kTile8;
   static constexpr int kMisc = kBars + A_COUNT * 8;
   static constexpr int kTok = (kMisc + 64 + 15) & ~15;  // float [2 warpgroups][128 rows]
-  static constexpr int kTotal = kTok + 2 * kBlk * 4;
+  static constexpr int kMeta = kTok + 2 * kBlk * 4;  // Meta [2][32]
+  static constexpr int kTotal = kMeta + 2 * kMetaTiles * 16;
   static constexpr int kAlloc = kTotal + 1024;  // room to align to 1024
   static constexpr int kFin = kK;    // the epilogue's [2][2][128] floats: K slot 0
   static constexpr int kStage = kV16;  // and O as bf16: V slot 0
@@ -133,6 +141,20 @@ __device__ __forceinline__ float lds_f(uint32_t addr) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
   return r;
 }
+__device__ __forceinline__ int lds_i(uint32_t addr) {
+  int r;
+  asm volatile("ld.shared.s32 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ int meta_half(int t) { return (t / kMetaTiles) & 1; }
 __device__ __forceinline__ void sts_f(uint32_t addr, float v) {
   asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -268,6 +290,8 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       uint32_t count = 1;
       if (i == A_Q_FULL) count = kSoftmax8;
       if (i >= A_V8_EMPTY && i < A_V8_EMPTY + kV8Slots) count = kConvert8;
+      if (i >= A_META_FULL && i < A_META_FULL + 2) count = 32;
+      if (i >= A_META_EMPTY && i < A_META_EMPTY + 2) count = kSoftmax8 + kConvert8;
       if (i >= A_PV_READY && i < A_PV_READY + kV16Slots) count = kSoftmax8 / 2 + kConvert8;
       mbar_init(&bars[i], count);
     }
@@ -347,6 +371,36 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
           if (last >= 0)
             mbar_wait_bounded(&bars[A_V8_FULL + sl], (last / kV8Slots) & 1, nullptr, kWait8);
         }
+      }
+    } else if (warp == 3) {
+      // ---------------- scales and valid counts ----------------
+      bool ok = true;
+      for (int b = 0; ok && b * kMetaTiles < n; ++b) {
+        const int t = b * kMetaTiles + lane;
+        int valid = kBlk;
+        float ks = 1.f, vs = 1.f;
+        if (t < n) {
+          const int blk = clamp_block(a, route[t]);
+          valid = a.block_valid[blk];
+          ks = checked_scale(a.k_scale[bh * a.max_blocks + blk], a.d_err);
+          vs = checked_scale(a.v_scale[bh * a.max_blocks + blk], a.d_err);
+          if (valid < 1 || valid > kBlk) {
+            report(a.d_err, BSA_DEV_BAD_VALID);
+            valid = valid < 1 ? 1 : kBlk;
+          }
+        }
+        if (b >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_META_EMPTY + (b & 1)],
+                                                         ((b >> 1) - 1) & 1, s_abort, kWait8));
+        if (!ok) break;
+        sts_v4(smem_u32(sm + L::kMeta) + ((b & 1) * kMetaTiles + lane) * 16,
+               make_uint4(__float_as_uint(ks), __float_as_uint(log2f(vs)),
+                          __float_as_uint(1.f / vs), static_cast<uint32_t>(valid)));
+        mbar_arrive(&bars[A_META_FULL + (b & 1)]);
+      }
+      if (!ok && lane == 0) {
+        report(a.d_err, BSA_DEV_WAIT_TIMEOUT);
+        *s_abort = 1;
       }
     } else if ((warp == 1 || warp == 2) && n > 0) {
       // ---------------- MMA issuers ----------------
@@ -429,11 +483,15 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     const uint32_t dst0 = smem_u32(sm + L::kV16) + (c >> 3) * (kBlk * 128) + r0 * 128 +
                           (((c & 7) ^ (r0 & 7)) << 4);
     bool ok = true;
-    int blk = n > 0 ? route[0] : 0;
     for (int t = 0; ok && t < n; ++t) {
-      int valid = a.block_valid[clamp_block(a, blk)];
-      valid = valid < 1 ? 1 : valid;
-      if (t + 1 < n) blk = route[t + 1];
+      if (t % kMetaTiles == 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_META_FULL + meta_half(t)],
+                                                       (t / (2 * kMetaTiles)) & 1, s_abort,
+                                                       kWait8));
+        if (!ok) break;
+      }
+      const int valid = lds_i(smem_u32(sm + L::kMeta) + (t % (2 * kMetaTiles)) * 16 + 12);
+      if (t % kMetaTiles == kMetaTiles - 1) mbar_arrive(&bars[A_META_EMPTY + meta_half(t)]);
       const int s8 = t % kV8Slots, sl = t % kV16Slots;
       // The whole warp passes each wait together: lanes that saw it complete at
       // different polls measured stale codes in their first load now and then.
@@ -482,16 +540,6 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     const int bar_in = 1 + (g ^ 1) * 4 + wq;
     const int bar_out = 1 + g * 4 + wq;
 
-    // Scales of this warpgroup's next tile, loaded a tile early.
-    int blk_ahead = (g + 2 < n) ? route[g + 2] : 0;
-    int valid_raw = kBlk;
-    float ks_raw = 1.f, vs_raw = 1.f;
-    if (g < n) {
-      const int blk = clamp_block(a, route[g]);
-      valid_raw = a.block_valid[blk];
-      ks_raw = a.k_scale[bh * a.max_blocks + blk];
-      vs_raw = a.v_scale[bh * a.max_blocks + blk];
-    }
     const float row_scale =
         split_query<D>(a, item, g, r, sm + L::kQ, tok) * a.scale_log2;
     fence_proxy_async_smem();
@@ -501,22 +549,16 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
     float l = 0.f;
     bool ok = true;
     for (int t = g; t < n; t += 2) {
-      int valid = valid_raw;
-      if (valid < 1 || valid > kBlk) {
-        report(a.d_err, BSA_DEV_BAD_VALID);
-        valid = valid < 1 ? 1 : kBlk;
-      }
-      const float factor = row_scale * checked_scale(ks_raw, a.d_err);
-      const float vs = checked_scale(vs_raw, a.d_err);
-      const float vlog2 = log2f(vs), vinv = 1.f / vs;
-      const int blk_ahead2 = (t + 4 < n) ? route[t + 4] : 0;
-      if (t + 2 < n) {
-        const int blk = clamp_block(a, blk_ahead);
-        valid_raw = a.block_valid[blk];
-        ks_raw = a.k_scale[bh * a.max_blocks + blk];
-        vs_raw = a.v_scale[bh * a.max_blocks + blk];
-      }
-      blk_ahead = blk_ahead2;
+      if (t % kMetaTiles == g && ok)
+        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_META_FULL + meta_half(t)],
+                                                       (t / (2 * kMetaTiles)) & 1, s_abort,
+                                                       kWait8));
+      uint4 meta = make_uint4(__float_as_uint(1.f), 0, __float_as_uint(1.f), kBlk);
+      if (ok) meta = lds_v4(smem_u32(sm + L::kMeta) + (t % (2 * kMetaTiles)) * 16);
+      if (t % kMetaTiles == kMetaTiles - 2 + g) mbar_arrive(&bars[A_META_EMPTY + meta_half(t)]);
+      const float factor = row_scale * __uint_as_float(meta.x);
+      const float vlog2 = __uint_as_float(meta.y), vinv = __uint_as_float(meta.z);
+      const int valid = static_cast<int>(meta.w);
       const uint32_t s_col = static_cast<uint32_t>(t % kS8Bufs) * 128;
 
       float s[kBlk];
