@@ -3,11 +3,11 @@
 // Per (batch, head, block) and tensor: A = max |r| over the block (r = the
 // turned key, or the value), scale = A / 448, code = e4m3(r * (448 / A)).  The
 // bytes it cannot do without are 2 read and 1 written per element.  A CTA
-// takes one block and a run of heads of one tensor; its 256 threads hold a
-// whole 128 x D tile in registers as bf16 (D/16 slots a row, rope.cuh), so
-// each element is read once: a first pass turns it and takes the maximum (and
-// the column sums of the keys), a second turns it again and rounds it.  The
-// angles belong to the row and are computed once for all heads of the run.
+// takes one block and a run of heads of one tensor; its 512 threads hold a
+// whole 128 x D tile in registers as turned fp32 values (D/16 slots a row,
+// rope.cuh), so each element is read and turned once, and load the next
+// head's tile while they reduce and round this one.  The angles belong to the
+// row and are computed once for all heads of the run.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "rope.cuh"
@@ -17,7 +17,8 @@ namespace bsa {
 
 bsa_status check_rope_chunk(int B, int Hh, int D, int T, int H, int W);
 
-constexpr int kApp8Threads = 256;
+constexpr int kApp8Threads = 512;
+constexpr int kApp8Warps = kApp8Threads / 32;
 
 struct Append8Args {
   RopeArgs rope;
@@ -33,9 +34,21 @@ struct Append8Args {
   int T, H, W;
 };
 
-__device__ __forceinline__ float finite_abs(float x) {
-  x = fabsf(x);
-  return x <= 3.402823466e38f ? x : 0.f;  // infinities and NaN do not set the scale
+// Largest of the warps' maxima, over all warps of the CTA.
+__device__ __forceinline__ float cta_max(const float* s_red) {
+  const float4* v = reinterpret_cast<const float4*>(s_red);
+  float m = 0.f;
+#pragma unroll
+  for (int w = 0; w < kApp8Warps / 4; ++w) {
+    const float4 x = v[w];
+    m = fmaxf(fmaxf(m, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+  }
+  return m;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  // Magnitudes: ordered as their bits.
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
 template <int D, int MODE, bool kMean>
@@ -44,7 +57,7 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
                                               float* s_sum) {
   constexpr int kSlots = D / 16, kVecs = D / 8;
   constexpr int kRowStep = kApp8Threads / kSlots;
-  constexpr int kRows = kBlk / kRowStep;  // rows per thread
+  constexpr int kRows = kBlk / kRowStep;  // rows per thread: 2, or 1 for D = 64
   const int slot = threadIdx.x % kSlots;
   const int row0 = threadIdx.x / kSlots;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -52,109 +65,136 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
   int va, vb;
   slot_vectors<MODE>(a.rope.P, slot, va, vb);
   SlotTrig g[kRows];
-  int tok[kRows];
+  const uint4* src[kRows];  // the row of head h0; null for a pad row
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    tok[i] = s_tok[row0 + i * kRowStep];
-    if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
-      slot_trig<MODE>(a.rope, token_pos(a.rope, bN, max(tok[i], 0)), slot, g[i]);
-      if (tok[i] < 0) g[i].n = 0;  // pad rows stay +0
-    }
+    const int tok = s_tok[row0 + i * kRowStep];
+    src[i] = tok < 0 ? nullptr : a.src[which] + ((bN + tok) * a.Hh + h0) * kVecs;
   }
-  const uint4* src = a.src[which];
-  for (int h = h0; h < h1; ++h) {
-    const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block +
-                          blockIdx.x;
-    uint4 x[kRows], y[kRows];
+  uint4 x[kRows], y[kRows];
+  auto load = [&](int h) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       x[i] = y[i] = make_uint4(0, 0, 0, 0);
-      if (MODE != kRopeHalfAny && tok[i] >= 0) {
-        const uint4* row = src + ((bN + tok[i]) * a.Hh + h) * kVecs;
-        x[i] = ld_nc_v4(row + va);
-        y[i] = ld_nc_v4(row + vb);
+      if (MODE != kRopeHalfAny && src[i] != nullptr) {
+        x[i] = ld_nc_v4(src[i] + (h - h0) * kVecs + va);
+        y[i] = ld_nc_v4(src[i] + (h - h0) * kVecs + vb);
       }
     }
-    auto value = [&](int i, float(&p)[8], float(&q)[8]) {
-      if (MODE == kRopeHalfAny) {
-        if (tok[i] >= 0) {
-          turn_slot_any(a.rope, token_pos(a.rope, bN, tok[i]), slot,
-                        reinterpret_cast<const __nv_bfloat16*>(
-                            src + ((bN + tok[i]) * a.Hh + h) * kVecs), p, q);
-        } else {
+  };
+  load(h0);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
-        }
-        return;
-      }
-      unpack8(x[i], p);
-      unpack8(y[i], q);
-      if (MODE != kRopeNone) turn_slot<MODE>(g[i], p, q);
-    };
-    float amax = 0.f;
-    float sum[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum[e] = 0.f;
+  for (int i = 0; i < kRows; ++i) {
+    if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
+      const int tok = s_tok[row0 + i * kRowStep];
+      slot_trig<MODE>(a.rope, token_pos(a.rope, bN, max(tok, 0)), slot, g[i]);
+      if (tok < 0) g[i].n = 0;  // pad rows stay +0
+    }
+  }
+  for (int h = h0; h < h1; ++h) {
+    const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block +
+                          blockIdx.x;
+    float p[kRows][8], q[kRows][8];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      float p[8], q[8];
-      value(i, p, q);
+      if (MODE == kRopeHalfAny) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        amax = fmaxf(amax, fmaxf(finite_abs(p[e]), finite_abs(q[e])));
-        if (kMean) {
-          sum[e] += p[e];
-          sum[8 + e] += q[e];
-        }
+        for (int e = 0; e < 8; ++e) p[i][e] = q[i][e] = 0.f;
+        if (src[i] != nullptr)
+          turn_slot_any(a.rope, token_pos(a.rope, bN, s_tok[row0 + i * kRowStep]), slot,
+                        reinterpret_cast<const __nv_bfloat16*>(src[i] + (h - h0) * kVecs), p[i],
+                        q[i]);
+      } else {
+        unpack8(x[i], p[i]);
+        unpack8(y[i], q[i]);
+        if (MODE != kRopeNone) turn_slot<MODE>(g[i], p[i], q[i]);
       }
     }
+    if (h + 1 < h1) load(h + 1);
+    float amax = 0.f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(p[i][e]), fabsf(q[i][e])));
+    }
+    amax = warp_max(amax);
+    // One barrier a head: the buffers alternate, so a head's are written again
+    // only after every thread has passed the next head's barrier.
+    float* red = s_red + (h & 1) * kApp8Warps;
+    float* sums = s_sum + (h & 1) * (kApp8Warps * D);
+    if (lane == 0) red[warp] = amax;
     if (kMean) {
       // Lanes with the same slot hold the same columns.
-#pragma unroll
-      for (int off = kSlots; off < 32; off <<= 1) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], off);
-      }
-    }
-    __syncthreads();  // the previous head's reads of s_red and s_sum are done
-    if (lane == 0) s_red[warp] = amax;
-    if (kMean && lane < kSlots) {
+      float sum[16];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s_sum[warp * D + va * 8 + e] = sum[e];
-        s_sum[warp * D + vb * 8 + e] = sum[8 + e];
+        sum[e] = p[0][e];
+        sum[8 + e] = q[0][e];
+#pragma unroll
+        for (int i = 1; i < kRows; ++i) {
+          sum[e] += p[i][e];
+          sum[8 + e] += q[i][e];
+        }
+      }
+      // Halve the columns a lane sums with each lane bit it is joined over: a
+      // lane ends with 16 / (32 / kSlots) columns.
+      int first = 0;
+#pragma unroll
+      for (int width = 8, off = 16; off >= kSlots; width >>= 1, off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int e = 0; e < width; ++e) {
+          const float give = up ? sum[e] : sum[e + width];
+          const float keep = up ? sum[e + width] : sum[e];
+          sum[e] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+        first += up ? width : 0;
+      }
+      constexpr int kLeft = 16 * kSlots / 32;
+#pragma unroll
+      for (int e = 0; e < kLeft; ++e) {
+        const int col = first + e;  // 0..7 of vector va, 8..15 of vb
+        sums[warp * D + (col < 8 ? va * 8 + col : vb * 8 + col - 8)] = sum[e];
       }
     }
     __syncthreads();
-    amax = s_red[0];
+    amax = cta_max(red);
+    if (amax > 3.402823466e38f) {
+      // An infinity: the scale is that of the largest finite magnitude.
+      amax = 0.f;
 #pragma unroll
-    for (int w = 1; w < kApp8Threads / 32; ++w) amax = fmaxf(amax, s_red[w]);
+      for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float u = fabsf(p[i][e]), v = fabsf(q[i][e]);
+          amax = fmaxf(amax, fmaxf(u <= 3.402823466e38f ? u : 0.f, v <= 3.402823466e38f ? v : 0.f));
+        }
+      }
+      amax = warp_max(amax);
+      __syncthreads();  // every thread has read the first maxima
+      if (lane == 0) red[warp] = amax;
+      __syncthreads();
+      amax = cta_max(red);
+    }
     amax = fmaxf(amax, kAmaxFloor);
     const float mul = kE4m3Max / amax;
     if (threadIdx.x == 0) a.scale[which][blk] = amax / kE4m3Max;
-    if (kMean) {
-      for (int c = threadIdx.x; c < D; c += kApp8Threads) {
-        float t = 0.f;
+    if (kMean && threadIdx.x < D) {
+      float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kApp8Threads / 32; ++w) t += s_sum[w * D + c];
-        a.kmean[blk * D + c] = t / static_cast<float>(valid);
-      }
+      for (int w = 0; w < kApp8Warps; ++w) t += sums[w * D + threadIdx.x];
+      a.kmean[blk * D + threadIdx.x] = t / static_cast<float>(valid);
     }
     uint8_t* dst = a.dst[which] + blk * (kBlk * D);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      float p[8], q[8];
-      value(i, p, q);
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        w[e] = pack_e4m3x2(p[4 * e] * mul, p[4 * e + 1] * mul) |
-               (pack_e4m3x2(p[4 * e + 2] * mul, p[4 * e + 3] * mul) << 16);
-        w[2 + e] = pack_e4m3x2(q[4 * e] * mul, q[4 * e + 1] * mul) |
-                   (pack_e4m3x2(q[4 * e + 2] * mul, q[4 * e + 3] * mul) << 16);
+        w[e] = pack_e4m3x2(p[i][4 * e] * mul, p[i][4 * e + 1] * mul) |
+               (pack_e4m3x2(p[i][4 * e + 2] * mul, p[i][4 * e + 3] * mul) << 16);
+        w[2 + e] = pack_e4m3x2(q[i][4 * e] * mul, q[i][4 * e + 1] * mul) |
+                   (pack_e4m3x2(q[i][4 * e + 2] * mul, q[i][4 * e + 3] * mul) << 16);
       }
       uint8_t* row = dst + (row0 + i * kRowStep) * D;
       if (MODE == kRopeHalf) {
@@ -168,13 +208,13 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kApp8Threads)
+__global__ void __launch_bounds__(kApp8Threads, 1)
 append8_kernel(Append8Args a) {
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
   __shared__ int s_tok[kBlk];
-  __shared__ float s_red[kApp8Threads / 32];
-  __shared__ float s_sum[kApp8Threads / 32 * D];
+  __shared__ __align__(16) float s_red[2 * kApp8Warps];
+  __shared__ float s_sum[2 * kApp8Warps * D];
   const int j = blockIdx.x;
   const int b = blockIdx.z / 2, which = blockIdx.z % 2;
   const int slot0 = j * kBlk;
@@ -245,12 +285,9 @@ extern "C" bsa_status bsa_kv8_append(bsa_kv_cache8* c, const void* k_tok, const 
   a.d_err = d_err;
   a.N = n;
   a.Hh = c->Hh;
-  // Two CTAs of this size fit an SM: enough of them for four waves, then as
-  // many heads as possible for each set of angles.
-  const long long others = 2LL * nb * c->B;
-  long long groups = (148 * 4 + others - 1) / others;
-  groups = groups > c->Hh ? c->Hh : groups;
-  a.heads = static_cast<int>((c->Hh + groups - 1) / groups);
+  // One CTA to an SM; its start and angles cost about one head's tile
+  // (2500 SM cycles against 2000).
+  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 1, 1.0);
   a.max_blocks = c->max_blocks;
   a.base_block = c->n_blocks;
   a.T = T;

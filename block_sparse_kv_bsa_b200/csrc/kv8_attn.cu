@@ -59,9 +59,9 @@ constexpr uint32_t kColO8 = 384;
 constexpr long long kWait8 = 1LL << 31;  // SM clocks (about a second)
 constexpr float kBias = 7.f;       // log2 of the weight of a fresh row maximum
 constexpr float kMoveAt = 15.f;    // a weight past 2^15 moves the reference
-// Registers per thread of each warpgroup: 64 + 2 * 176 + 96 = 4 * 128, what
+// Registers per thread of each warpgroup: 64 + 2 * 184 + 80 = 4 * 128, what
 // the block is launched with.
-constexpr int kRegsIssue = 64, kRegsSoftmax = 176, kRegsConvert = 96;
+constexpr int kRegsIssue = 64, kRegsSoftmax = 184, kRegsConvert = 80;
 
 constexpr int kMetaTiles = 32;  // tiles of a half of the metadata ring
 

@@ -207,15 +207,6 @@ rope_blocks_kernel(RopeBlocksArgs a) {
   }
 }
 
-// Heads per CTA: enough CTAs to fill the GPU, then as many heads as possible
-// for each set of angles.
-static int heads_per_cta(long long other_ctas, int Hh) {
-  const long long want = 148 * 4;
-  long long groups = (want + other_ctas - 1) / other_ctas;
-  if (groups > Hh) groups = Hh;
-  return static_cast<int>((Hh + groups - 1) / groups);
-}
-
 template <int D>
 static bsa_status launch_tokens(int mode, const RopeTokensArgs& a, int B, cudaStream_t s) {
   constexpr int kToks = kRopeThreads / (D / 16);
@@ -312,7 +303,7 @@ extern "C" bsa_status bsa_rope(const void* x_tok, void* y_tok, int B, int Hh, in
   a.N = T * H * W;
   a.Hh = Hh;
   const int toks = kRopeThreads / (D / 16);
-  a.heads = heads_per_cta(static_cast<long long>((a.N + toks - 1) / toks) * B, Hh);
+  a.heads = heads_per_cta(static_cast<long long>((a.N + toks - 1) / toks) * B, Hh, 3, 2.0);
   return D == 128 ? launch_tokens<128>(mode, a, B, as_stream(stream))
                   : launch_tokens<64>(mode, a, B, as_stream(stream));
 }
@@ -337,7 +328,7 @@ extern "C" bsa_status bsa_tokens_to_blocks_rope(const void* x_tok, void* x_blk, 
   a.N = n;
   a.Hh = Hh;
   a.tensors = 1;
-  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh);
+  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh, 2, 2.0);
   a.blk_stride = nb;
   a.T = T;
   a.H = H;
@@ -376,7 +367,7 @@ extern "C" bsa_status bsa_kv_append_rope(bsa_kv_cache* c, const void* k_tok, con
   a.N = n;
   a.Hh = c->Hh;
   a.tensors = 2;
-  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh);
+  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 2, 2.0);
   a.blk_stride = c->max_blocks;
   a.base_block = c->n_blocks;
   a.T = T;

@@ -11,7 +11,7 @@
 //                 and fetches each element's partner by itself (kHalfAny)
 // The angle is exact: phase[i] is the pair's frequency as a 64-bit fraction
 // of a turn, p * phase mod 2^64 the fraction turned, whose top 32 bits (an
-// error below 2^-32 turn) go to sincospif as half turns in [-1, 1).
+// error below 2^-32 turn) give its sine and cosine.
 #pragma once
 
 #include "common.cuh"
@@ -55,6 +55,28 @@ __device__ __forceinline__ TokenPos token_pos(const RopeArgs& r, long long bN, i
   return t;
 }
 
+// cos and sin of a fraction of a turn (its top 32 bits).  The nearest quarter
+// turn is split off exactly in integers; what is left, |x| <= pi / 4, goes into
+// the Taylor series of sin through x^9 and of cos through x^8 (truncation
+// below 2^-25), about 20 instructions.
+__device__ __forceinline__ void turn_trig(uint32_t turn, float& c, float& s) {
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const int32_t rest = static_cast<int32_t>(turn - (quarter << 30));
+  const float x = static_cast<float>(rest) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float x2 = x * x;
+  float ps = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);
+  ps = fmaf(ps, x2, 8.3333333e-3f);
+  ps = fmaf(ps, x2, -1.6666667e-1f);
+  const float sn = fmaf(ps * x2, x, x);
+  float pc = fmaf(x2, 2.4801587e-5f, -1.3888889e-3f);
+  pc = fmaf(pc, x2, 4.1666667e-2f);
+  pc = fmaf(pc, x2, -0.5f);
+  const float cs = fmaf(pc, x2, 1.f);
+  const float u = quarter & 1 ? cs : sn, v = quarter & 1 ? sn : cs;
+  s = __uint_as_float(__float_as_uint(u) ^ ((quarter & 2) << 30));
+  c = __uint_as_float(__float_as_uint(v) ^ (((quarter + 1) & 2) << 30));
+}
+
 // cos and sin of pair i (amplitude and direction applied).
 __device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, int i, float& c,
                                           float& s) {
@@ -62,8 +84,7 @@ __device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, 
   const long long p = static_cast<long long>(ax == 0 ? t.p[0] : (ax == 1 ? t.p[1] : t.p[2])) +
                       (ax == 0 ? r.o0 : (ax == 1 ? r.o1 : r.o2));
   const uint64_t turn = static_cast<uint64_t>(p) * __ldg(r.phase + i);
-  const int32_t hi = static_cast<int32_t>(turn >> 32);
-  sincospif(static_cast<float>(hi) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+  turn_trig(static_cast<uint32_t>(turn >> 32), c, s);
   c *= r.amp;
   s *= r.inverse ? -r.amp : r.amp;
 }
@@ -155,6 +176,24 @@ __device__ __forceinline__ void turn_slot_any(const RopeArgs& r, const TokenPos&
       if (e == k + 8) b[k] = v;
     }
   }
+}
+
+// Heads per CTA for a grid of `others` CTAs per run of heads, `per_sm` of them
+// resident on each of 148 SMs: the run whose waves of CTAs take the fewest
+// head times, a CTA's start and angles counting as `start` heads.
+inline int heads_per_cta(long long others, int Hh, int per_sm, double start) {
+  int best = 1;
+  double best_cost = -1.0;
+  for (int heads = 1; heads <= Hh && heads <= 64; ++heads) {
+    const long long ctas = others * ((Hh + heads - 1) / heads);
+    const long long waves = (ctas + 148 * per_sm - 1) / (148 * per_sm);
+    const double cost = static_cast<double>(waves) * (heads + start);
+    if (best_cost < 0.0 || cost < best_cost) {
+      best_cost = cost;
+      best = heads;
+    }
+  }
+  return best;
 }
 
 // Checks a descriptor and fills the kernel's arguments; `mode` is how the
