@@ -185,13 +185,22 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _dev(device) -> torch.device:
     """A device with an explicit index (``cuda`` -> ``cuda:<current>``)."""
+    if isinstance(device, torch.device) and device.index is not None:
+        return device
     d = torch.device(device)
     if d.type == "cuda" and d.index is None:
         d = torch.device("cuda", torch.cuda.current_device())
     return d
 
 
+# The current stream's handle without building a Stream object (2.4 us less on
+# a call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device) -> ctypes.c_void_p:
+    if _raw_stream is not None and isinstance(device, torch.device) and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -730,6 +739,9 @@ class Rope:
         self.pairs, self.layout, self.amplitude = pairs, layout, float(amplitude)
         self.device = _dev(device)
         self.phase = torch.from_numpy(phase).to(self.device)
+        p = pairs + (0,) * (3 - len(pairs))
+        self._struct = CRope(None, (ctypes.c_int32 * 3)(*p), len(pairs), ROPE_LAYOUTS[layout], 0,
+                             self.amplitude, None, (ctypes.c_int32 * 3)(0, 0, 0))
 
     @property
     def n_axes(self) -> int:
@@ -739,13 +751,17 @@ class Rope:
                  inverse: bool = False) -> CRope:
         if pos is not None:
             _need(pos, "pos", torch.int32, self.device, (self.n_axes, B, N))
-        o = tuple(int(x) for x in origin)
-        if len(o) != 3 or not all(-(1 << 31) <= x < (1 << 31) for x in o):
-            raise ValueError("origin must be three int32 positions")
-        p = self.pairs + (0,) * (3 - len(self.pairs))
-        return CRope(self.phase.data_ptr(), (ctypes.c_int32 * 3)(*p), self.n_axes,
-                     ROPE_LAYOUTS[self.layout], int(bool(inverse)), self.amplitude,
-                     None if pos is None else pos.data_ptr(), (ctypes.c_int32 * 3)(*o))
+        c = CRope.from_buffer_copy(self._struct)
+        c.phase = self.phase.data_ptr()
+        if pos is not None:
+            c.pos = pos.data_ptr()
+        c.inverse = int(bool(inverse))
+        o0, o1, o2 = origin
+        for x in (o0, o1, o2):
+            if not -(1 << 31) <= x < (1 << 31):
+                raise ValueError("origin must be three int32 positions")
+        c.origin[0], c.origin[1], c.origin[2] = int(o0), int(o1), int(o2)
+        return c
 
 
 def _on(device, fn: str, *args):
