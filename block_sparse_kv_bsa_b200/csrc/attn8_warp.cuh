@@ -1,10 +1,11 @@
 // attn8_warp.cuh - one warp's attention of 16 query rows over keys of the
-// 8-bit cache, on mma.sync m16n8k16 (f16 in, fp32 out), K and V straight from
-// global memory into registers.
+// 8-bit cache, on mma.sync m16n8k16 (f16 in, fp32 out), K and V from tiles in
+// shared memory in TMA's swizzle (16-byte chunk c of row r at chunk c ^ (r % 8)
+// of 128-byte rows, c ^ (r / 2 % 4) of 64-byte rows).
 //
 // Fragment maps (g = lane / 4, t = lane % 4), chosen so that every lane's
-// loads are whole 16-byte (V at D = 64: 8-byte) pieces and each warp-wide load
-// covers whole 32-byte sectors:
+// loads are whole 16-byte (V at D = 64: 8-byte) pieces and eight lanes never
+// meet in a bank:
 //   Q K^T  the k index of step ks is d = (ks / 4) * 64 + t * 16 + (ks % 4) * 4
 //          + {0, 1 | 2, 3}: a lane holds 16 consecutive d of key g a load.
 //   P V    the n index of tile nt is d = g * (D / 8) + nt: a lane holds D / 8
@@ -39,6 +40,21 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Loads the compiler keeps in their place among the barrier operations.
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
+  return r;
+}
+
 // 2^e as a float, e within the normal range.
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -64,6 +80,10 @@ struct AttnWarp {
   float row_scale[2];  // query row scale * sm_scale * log2 e, rows g and g + 8
   float o[kTiles][4];
   float m[2], l[2];
+
+  static __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  }
 
   struct Keys {  // 16 keys
     uint4 k[2][kKLoads];         // key g of each half
@@ -125,35 +145,40 @@ struct AttnWarp {
     }
   }
 
-  // Load keys [first, first + 16) of a block; those at or past `valid` read
-  // as zero.
-  __device__ __forceinline__ void load_keys(const uint8_t* kb, const uint8_t* vb, int first,
-                                            int valid, Keys& x) const {
+  // Keys [first, first + 16) of the tiles at shared addresses kt and vt; values
+  // at or past `valid` read as zero (their weights are zero, but a NaN code
+  // would survive that).
+  __device__ __forceinline__ void load_keys(uint32_t kt, uint32_t vt, int first, int valid,
+                                            Keys& x) const {
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int key = first + n * 8 + g;
 #pragma unroll
-      for (int i = 0; i < kKLoads; ++i)
-        x.k[n][i] = key < valid ? ld_nc_v4(kb + key * D + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kKLoads; ++i) x.k[n][i] = lds128(kt + chunk_at(key, i * 4 + t));
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const int key = first + (n / 2) * 8 + 2 * t + (n & 1);
       if (D == 128) {
-        const uint4 u = key < valid ? ld_nc_v4(vb + key * D + g * 16) : make_uint4(0, 0, 0, 0);
+        const uint4 u = lds128(vt + chunk_at(key, g));
         x.v[n][0] = u.x;
         x.v[n][1] = u.y;
         x.v[n][kVWords - 2] = u.z;
         x.v[n][kVWords - 1] = u.w;
       } else {
-        uint2 u = make_uint2(0, 0);
-        if (key < valid)
-          asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                       : "=r"(u.x), "=r"(u.y)
-                       : "l"(vb + key * D + g * 8));
+        const uint2 u = lds64(vt + chunk_at(key, g >> 1) + (g & 1) * 8);
         x.v[n][0] = u.x;
         x.v[n][1] = u.y;
+      }
+    }
+    if (first + 16 > valid) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (first + (n / 2) * 8 + 2 * t + (n & 1) >= valid) {
+#pragma unroll
+          for (int w = 0; w < kVWords; ++w) x.v[n][w] = 0;
+        }
       }
     }
   }

@@ -45,6 +45,21 @@
 
 namespace bsa {
 
+// 2D map over e4m3 [rows, D]: a 128-row tile per box, swizzled over its row.
+bool make_map8(CUtensorMap* m, const void* base, long long rows, int D) {
+  auto enc = get_encode();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(D), kBlk};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 constexpr int kThreads8 = 512;
@@ -732,21 +747,7 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
   }
 }
 
-// 2D maps: e4m3 [rows, D], a tile per box; bf16 [rows, D], boxes of 64 columns.
-bool make_map8(CUtensorMap* m, const void* base, long long rows, int D) {
-  auto enc = get_encode();
-  if (enc == nullptr) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(D), kBlk};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
+// 2D map over bf16 [rows, D]: boxes of 128 rows x 64 columns.
 bool make_map_out(CUtensorMap* m, const void* base, long long rows, int D) {
   auto enc = get_encode();
   if (enc == nullptr) return false;

@@ -4,10 +4,11 @@
 // The rows of one cache head are its n_tok * group query rows, 16 to a tile
 // (mma.sync, attn8_warp.cuh).  With so few rows the call is bound by reading
 // the cache once (1 byte an element of K and V), so the blocks are split over
-// enough CTAs to fill the GPU; each warp of a CTA streams its own 16-key
-// steps with the next step's loads in flight, the warps join through shared
-// memory and the splits through a workspace and a second small kernel, always
-// in the same order.
+// the SMs and each CTA streams its share through a ring of K and V tiles that
+// TMA keeps full (192 KB: the 50 KB or so that an SM must have in flight to
+// draw its part of the memory rate, several times over).  Eight warps take 16
+// keys each of every block; they join through shared memory, and the splits
+// through a workspace and a second small kernel, always in the same order.
 #include "common.cuh"
 #include "attn8_warp.cuh"
 #include "tma_host.cuh"
@@ -16,16 +17,30 @@ namespace bsa {
 
 
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = kDecWarps * 32;
-constexpr int kDecSlots = 296;     // CTAs resident at once: two on each of 148 SMs
+constexpr int kDecWarps = 8;                          // consumers: 16 keys of each block
+constexpr int kDecThreads = kDecWarps * 32 + 32;      // and one producer warp
+constexpr int kDecSlots = 148;     // CTAs resident at once: one on each SM
 constexpr int kDecMaxRows = 128;   // query rows of one cache head
-constexpr int kDecChunk = kDecThreads;  // blocks whose metadata is staged at a time
+constexpr int kDecMaxSplit = 148;
+constexpr long long kDecWait = 1LL << 31;  // SM clocks (about a second)
+
+template <int D>
+struct DecodeLayout {
+  static constexpr int kTile = kBlk * D;
+  static constexpr int kStages = D == 128 ? 6 : 12;
+  static constexpr int kRing = 0;                              // [stage][K, V]
+  static constexpr int kBars = kRing + kStages * 2 * kTile;    // full, empty per stage
+  static constexpr int kMeta = kBars + kStages * 16;           // float4 per stage
+  static constexpr int kMl = kMeta + kStages * 16;             // float [warps][16][2]
+  static constexpr int kMisc = kMl + kDecWarps * 16 * 8;
+  static constexpr int kAlloc = kMisc + 16 + 1024;
+  static constexpr int kOut = kRing;                           // float [warps][16][D] at the end
+  static_assert(kDecWarps * 16 * D * 4 <= kStages * 2 * kTile, "warps' O fits the ring");
+  static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
+};
 
 struct Decode8Args {
   const __nv_bfloat16* q;
-  const uint8_t* k;
-  const uint8_t* v;
   const float* k_scale;
   const float* v_scale;
   const int32_t* block_valid;
@@ -50,27 +65,34 @@ __device__ __forceinline__ long long query_row(const Decode8Args& a, long long b
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDecThreads, 2)
-decode8_kernel(Decode8Args a) {
+__global__ void __launch_bounds__(kDecThreads, 1)
+decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               Decode8Args a) {
+  using L = DecodeLayout<D>;
+  using W = AttnWarp<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_u32(sm);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);
+  uint64_t* empty = full + L::kStages;
+  volatile int* s_abort = reinterpret_cast<volatile int*>(sm + L::kMisc);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kDecWarps);
+    }
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
-  using W = AttnWarp<D>;
-  __shared__ int s_blk[kDecChunk];
-  __shared__ int s_valid[kDecChunk];
-  __shared__ float s_ks[kDecChunk], s_vlog2[kDecChunk], s_vinv[kDecChunk];
-  __shared__ float s_o[kDecWarps][16][D];
-  __shared__ float s_ml[kDecWarps][16][2];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int split = blockIdx.y;
   const long long item = blockIdx.x;
   const long long bh = item / a.tiles;
   const int tile = static_cast<int>(item % a.tiles);
-  const int r0 = tile * 16 + g;
-
-  W w;
-  w.init();
-  w.load_q(r0 < a.rows ? a.q + query_row(a, bh, r0) * D : nullptr,
-           r0 + 8 < a.rows ? a.q + query_row(a, bh, r0 + 8) * D : nullptr, a.scale_log2);
 
   int n = a.n_sel;
   if (a.cnt != nullptr) {
@@ -81,82 +103,121 @@ decode8_kernel(Decode8Args a) {
     }
   }
   const int per = (n + a.n_split - 1) / a.n_split;
-  const int e0 = min(n, split * per), e1 = min(n, e0 + per);
-  for (int c0 = e0; c0 < e1; c0 += kDecChunk) {
-    const int count = min(kDecChunk, e1 - c0);
-    __syncthreads();
-    if (threadIdx.x < count) {
-      int blk = c0 + threadIdx.x;
-      if (a.idx != nullptr) {
-        blk = a.idx[bh * a.n_sel + blk];
-        if (blk < 0 || blk >= a.n_blocks) {
-          report(a.d_err, BSA_DEV_BAD_INDEX);
-          blk = 0;
-        }
-      }
-      int valid = a.block_valid[blk];
-      if (valid < 1 || valid > kBlk) {
-        report(a.d_err, BSA_DEV_BAD_VALID);
-        valid = valid < 1 ? 1 : kBlk;
-      }
-      const long long at = bh * a.max_blocks + blk;
-      const float vs = checked_scale(a.v_scale[at], a.d_err);
-      s_blk[threadIdx.x] = blk;
-      s_valid[threadIdx.x] = valid;
-      s_ks[threadIdx.x] = checked_scale(a.k_scale[at], a.d_err);
-      s_vlog2[threadIdx.x] = log2f(vs);
-      s_vinv[threadIdx.x] = 1.f / vs;
-    }
-    __syncthreads();
-    // Step u: keys (u % 8) * 16 .. of entry u / 8.
-    const int units = count * 8;
-    auto load = [&](int u, typename W::Keys& x) {
-      const long long at = (bh * a.max_blocks + s_blk[u / 8]) * (kBlk * D);
-      w.load_keys(a.k + at, a.v + at, (u % 8) * 16, s_valid[u / 8], x);
-    };
-    typename W::Keys cur, next;
-    if (warp < units) load(warp, cur);
-    for (int u = warp; u < units; u += kDecWarps) {
-      if (u + kDecWarps < units) load(u + kDecWarps, next);
-      const int e = u / 8;
-      if ((u % 8) * 16 < s_valid[e])
-        w.step(cur, (u % 8) * 16, s_valid[e], s_ks[e], s_vlog2[e], s_vinv[e]);
-      cur = next;
-    }
-  }
-  w.finish();
+  const int e0 = min(n, split * per), count = min(n - e0, per);
 
-  // Join the warps.
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-#pragma unroll
-    for (int i = 0; i < W::kTiles; ++i) {
-      s_o[warp][g + 8 * r][(2 * t) * (D / 8) + i] = w.o[i][2 * r];
-      s_o[warp][g + 8 * r][(2 * t + 1) * (D / 8) + i] = w.o[i][2 * r + 1];
+  W w;
+  w.init();
+  bool ok = true;
+  if (warp == kDecWarps) {
+    // ---------------- producer: metadata of 32 blocks at a time, then their tiles
+    int issued = 0;
+    for (int c0 = 0; ok && c0 < count; c0 += 32) {
+      int blk = e0 + c0 + lane, valid = kBlk;
+      float ks = 1.f, vs = 1.f;
+      if (c0 + lane < count) {
+        if (a.idx != nullptr) {
+          blk = a.idx[bh * a.n_sel + blk];
+          if (blk < 0 || blk >= a.n_blocks) {
+            report(a.d_err, BSA_DEV_BAD_INDEX);
+            blk = 0;
+          }
+        }
+        valid = a.block_valid[blk];
+        if (valid < 1 || valid > kBlk) {
+          report(a.d_err, BSA_DEV_BAD_VALID);
+          valid = valid < 1 ? 1 : kBlk;
+        }
+        ks = checked_scale(a.k_scale[bh * a.max_blocks + blk], a.d_err);
+        vs = checked_scale(a.v_scale[bh * a.max_blocks + blk], a.d_err);
+      }
+      const float vlog2 = log2f(vs), vinv = 1.f / vs;
+      for (int i = 0; ok && i < 32 && c0 + i < count; ++i) {
+        const int u = c0 + i, st = u % L::kStages;
+        if (u >= L::kStages)
+          ok = __all_sync(0xffffffffu, mbar_wait_bounded(&empty[st], ((u / L::kStages) - 1) & 1,
+                                                         s_abort, kDecWait));
+        if (!ok) break;
+        if (lane == i) {
+          float4* meta = reinterpret_cast<float4*>(sm + L::kMeta) + st;
+          *meta = make_float4(ks, vlog2, vinv, __int_as_float(valid));
+          const int row = static_cast<int>((bh * a.max_blocks + blk) * kBlk);
+          uint8_t* dst = sm + L::kRing + st * 2 * L::kTile;
+          mbar_expect_tx(&full[st], 2 * L::kTile);
+          tma_load_2d(dst, &tm_k, 0, row, &full[st]);
+          tma_load_2d(dst + L::kTile, &tm_v, 0, row, &full[st]);
+        }
+        __syncwarp();
+        issued = u + 1;
+      }
     }
-    if (t == 0) {
-      s_ml[warp][g + 8 * r][0] = w.m[r];
-      s_ml[warp][g + 8 * r][1] = w.l[r];
+    // Copies in flight land before the ring is reused or the CTA exits.
+    for (int u = max(0, issued - L::kStages); u < issued; ++u)
+      mbar_wait_bounded(&full[u % L::kStages], (u / L::kStages) & 1, nullptr, kDecWait);
+  } else {
+    const int r0 = tile * 16 + g;
+    w.load_q(r0 < a.rows ? a.q + query_row(a, bh, r0) * D : nullptr,
+             r0 + 8 < a.rows ? a.q + query_row(a, bh, r0 + 8) * D : nullptr, a.scale_log2);
+    for (int u = 0; ok && u < count; ++u) {
+      const int st = u % L::kStages;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_bounded(&full[st], (u / L::kStages) & 1, s_abort, kDecWait));
+      if (!ok) break;
+      const uint4 meta = lds128(base + L::kMeta + st * 16);
+      const int valid = static_cast<int>(meta.w);
+      if (warp * 16 < valid) {
+        typename W::Keys x;
+        const uint32_t kt = base + L::kRing + st * 2 * L::kTile;
+        w.load_keys(kt, kt + L::kTile, warp * 16, valid, x);
+        w.step(x, warp * 16, valid, __uint_as_float(meta.x), __uint_as_float(meta.y),
+               __uint_as_float(meta.z));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    w.finish();
+  }
+  if (!ok && lane == 0) {
+    report(a.d_err, BSA_DEV_WAIT_TIMEOUT);
+    *s_abort = 1;
+  }
+
+  // Join the warps: the ring is empty (every tile issued has been read).
+  __syncthreads();
+  float* s_o = reinterpret_cast<float*>(sm + L::kOut);  // [warp][16][D]
+  float* s_ml = reinterpret_cast<float*>(sm + L::kMl);  // [warp][16][2]
+  if (warp < kDecWarps) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float* o = s_o + (warp * 16 + g + 8 * r) * D;
+#pragma unroll
+      for (int i = 0; i < W::kTiles; ++i) {
+        o[(2 * t) * (D / 8) + i] = w.o[i][2 * r];
+        o[(2 * t + 1) * (D / 8) + i] = w.o[i][2 * r + 1];
+      }
+      if (t == 0) {
+        s_ml[(warp * 16 + g + 8 * r) * 2] = w.m[r];
+        s_ml[(warp * 16 + g + 8 * r) * 2 + 1] = w.l[r];
+      }
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 16 * D; i += kDecThreads) {
+  const int rows = min(16, a.rows - tile * 16);
+  for (int i = threadIdx.x; i < rows * D; i += kDecThreads) {
     const int r = i / D, d = i % D;
-    const int row = tile * 16 + r;
-    if (row >= a.rows) break;
-    float m = s_ml[0][r][0];
+    float m = -INFINITY;
 #pragma unroll
-    for (int k = 1; k < kDecWarps; ++k) m = fmaxf(m, s_ml[k][r][0]);
+    for (int k = 0; k < kDecWarps; ++k) m = fmaxf(m, s_ml[(k * 16 + r) * 2]);
     float l = 0.f, o = 0.f;
 #pragma unroll
     for (int k = 0; k < kDecWarps; ++k) {
-      const float f = s_ml[k][r][0] == -INFINITY ? 0.f : ex2_approx(s_ml[k][r][0] - m);
-      l = fmaf(s_ml[k][r][1], f, l);
-      o = fmaf(s_o[k][r][d], f, o);
+      const float mk = s_ml[(k * 16 + r) * 2];
+      const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - m);
+      l = fmaf(s_ml[(k * 16 + r) * 2 + 1], f, l);
+      o = fmaf(s_o[(k * 16 + r) * D + d], f, o);
     }
     if (a.n_split == 1) {
       const bool have = m > -INFINITY;
-      const long long out = query_row(a, bh, row);
+      const long long out = query_row(a, bh, tile * 16 + r);
       a.o[out * D + d] = __float2bfloat16(have ? o / l : 0.f);
       if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else {
@@ -178,7 +239,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 decode8_join_kernel(Decode8Args a) {
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
-  __shared__ float s_w[kDecSlots];
+  __shared__ float s_w[kDecMaxSplit];
   __shared__ float s_red[2][kJoinThreads / 32];
   __shared__ float s_acc[kJoinThreads];
   const int row = blockIdx.y;
@@ -226,7 +287,8 @@ decode8_join_kernel(Decode8Args a) {
 }
 
 // Splits of n_sel blocks: the count whose waves over the resident CTAs leave
-// the fewest idle (a split is a wave's share of the blocks), fewest first.
+// the fewest idle (a split is a wave's share of the blocks; a CTA's start and
+// join count as two blocks), fewest first.
 static int most_splits(long long items, int n_sel) {
   long long most = kDecSlots / items;
   if (most < 8) most = 8;
@@ -239,7 +301,7 @@ static int split_count(long long items, int n_sel) {
   double best_cost = 1e30;
   for (int n = 1; n <= most; ++n) {
     const long long waves = (items * n + kDecSlots - 1) / kDecSlots;
-    const double cost = static_cast<double>(waves) * ((n_sel + n - 1) / n) * (1.0 + 0.0001 * n);
+    const double cost = static_cast<double>(waves) * ((n_sel + n - 1) / n + 2) * (1.0 + 0.0001 * n);
     if (cost < best_cost) {
       best_cost = cost;
       best = n;
@@ -275,10 +337,17 @@ static bsa_status decode_shape(int B, int Hq, int Hh, int D, int n_tok, int n_se
 }
 
 template <int D>
-static bsa_status launch_decode(const Decode8Args& a, long long bh, cudaStream_t s) {
-  const long long items = bh * a.tiles;
-  BSA_TRY(launch_pdl(decode8_kernel<D>, dim3(static_cast<unsigned>(items), a.n_split),
-                     dim3(kDecThreads), 0, s, a));
+static bsa_status launch_decode(const Decode8Args& a, const bsa_kv_cache8* c, cudaStream_t s) {
+  CUtensorMap tk, tv;
+  const long long bh = static_cast<long long>(c->B) * c->Hh;
+  const long long crows = bh * c->max_blocks * kBlk;
+  if (!make_map8(&tk, c->k, crows, D) || !make_map8(&tv, c->v, crows, D)) return BSA_ERR_CUDA;
+  const int smem = DecodeLayout<D>::kAlloc;
+  if (cudaFuncSetAttribute(decode8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+      cudaSuccess)
+    return BSA_ERR_CUDA;
+  BSA_TRY(launch_pdl(decode8_kernel<D>, dim3(static_cast<unsigned>(bh * a.tiles), a.n_split),
+                     dim3(kDecThreads), static_cast<size_t>(smem), s, tk, tv, a));
   if (a.n_split == 1) return BSA_OK;
   return launch_pdl(decode8_join_kernel<D>, dim3(static_cast<unsigned>(bh), a.rows),
                     dim3(kJoinThreads), 0, s, a);
@@ -315,12 +384,12 @@ extern "C" bsa_status bsa_kv8_attn_decode(const void* q_tok, const bsa_kv_cache8
   const int n_sel = idx != nullptr ? max_sel : c->n_blocks;
   DecodeShape sh;
   BSA_TRY(decode_shape(c->B, Hq, c->Hh, c->D, n_tok, n_sel, &sh));
+  const long long crows = static_cast<long long>(c->B) * c->Hh * c->max_blocks * kBlk;
+  if (crows >= (1LL << 31)) return BSA_ERR_SHAPE;
   if (sh.bytes > 0 && (workspace == nullptr || ws_bytes < sh.bytes)) return BSA_ERR_CAPACITY;
   if (!device_is_sm100()) return BSA_ERR_UNSUPPORTED;
   Decode8Args a{};
   a.q = static_cast<const __nv_bfloat16*>(q_tok);
-  a.k = static_cast<const uint8_t*>(c->k);
-  a.v = static_cast<const uint8_t*>(c->v);
   a.k_scale = c->k_scale;
   a.v_scale = c->v_scale;
   a.block_valid = c->block_valid;
@@ -342,7 +411,6 @@ extern "C" bsa_status bsa_kv8_attn_decode(const void* q_tok, const bsa_kv_cache8
   a.max_blocks = c->max_blocks;
   a.n_blocks = c->n_blocks;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
-  const long long bh = static_cast<long long>(c->B) * c->Hh;
-  return c->D == 128 ? launch_decode<128>(a, bh, as_stream(stream))
-                     : launch_decode<64>(a, bh, as_stream(stream));
+  return c->D == 128 ? launch_decode<128>(a, c, as_stream(stream))
+                     : launch_decode<64>(a, c, as_stream(stream));
 }
