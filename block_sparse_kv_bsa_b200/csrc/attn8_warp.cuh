@@ -150,6 +150,10 @@ struct AttnWarp {
   // would survive that).
   __device__ __forceinline__ void load_keys(uint32_t kt, uint32_t vt, int first, int valid,
                                             Keys& x) const {
+    if (first >= valid) {
+      x = Keys{};
+      return;
+    }
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -183,34 +187,43 @@ struct AttnWarp {
     }
   }
 
-  // One step: 16 keys of a block with scales kscale (key), log2 v and 1 / v.
-  __device__ __forceinline__ void step(const Keys& x, int first, int valid, float kscale,
-                                       float vlog2, float vinv) {
+  // One step: keys [first, first + 16) of G blocks at once (their products and
+  // exponentials are independent, one maximum and one rescale serve all).
+  // meta[b] = (key scale, log2 v, 1 / v, valid rows as int) of block b; a block
+  // with no valid key in the step must hold zeros in x[b].
+  template <int G>
+  __device__ __forceinline__ void step(const Keys (&x)[G], int first, const uint4 (&meta)[G]) {
     const int t = threadIdx.x % 4;
-    float s[2][4];
+    float s[2 * G][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < 2 * G; ++n) {
       s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    }
 #pragma unroll
-      for (int i = 0; i < kKLoads; ++i) {
-        const uint32_t w[4] = {x.k[n][i].x, x.k[n][i].y, x.k[n][i].z, x.k[n][i].w};
+    for (int i = 0; i < kKLoads; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_f16(s[n], q[i * 4 + e], e4m3_lo_f16x2(w[e]), e4m3_hi_f16x2(w[e]));
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int n = 0; n < 2 * G; ++n) {
+          const uint4& k = x[n / 2].k[n & 1][i];
+          const uint32_t w = e == 0 ? k.x : (e == 1 ? k.y : (e == 2 ? k.z : k.w));
+          mma_f16(s[n], q[i * 4 + e], e4m3_lo_f16x2(w), e4m3_hi_f16x2(w));
+        }
       }
     }
     float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < 2 * G; ++n) {
+      const float ks = __uint_as_float(meta[n / 2].x), vlog2 = __uint_as_float(meta[n / 2].y);
+      const int valid = static_cast<int>(meta[n / 2].w);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = e / 2;
-        const int key = first + n * 8 + 2 * t + (e & 1);
-        s[n][e] = key < valid ? fmaf(s[n][e], row_scale[r] * kscale, vlog2) : -INFINITY;
+        const int key = first + (n & 1) * 8 + 2 * t + (e & 1);
+        s[n][e] = key < valid ? fmaf(s[n][e], row_scale[r] * ks, vlog2) : -INFINITY;
         mx[r] = fmaxf(mx[r], s[n][e]);
       }
     }
-    float sum[2] = {0.f, 0.f};
     bool move = false;
     float fix[2] = {1.f, 1.f}, ref[2];
 #pragma unroll
@@ -235,28 +248,33 @@ struct AttnWarp {
         o[i][3] *= fix[1];
       }
     }
-    uint32_t p[4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int b = 0; b < G; ++b) {
+      uint32_t p[4];
+      const float vinv = __uint_as_float(meta[b].z);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float e0 = ex2_approx(s[n][2 * r] - ref[r]), e1 = ex2_approx(s[n][2 * r + 1] - ref[r]);
-        sum[r] += e0 + e1;
-        p[n * 2 + r] = pack_f16x2(e0, e1);
-      }
-    }
-    l[0] = fmaf(sum[0], vinv, l[0]);
-    l[1] = fmaf(sum[1], vinv, l[1]);
+        float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kVWords; ++w) {
-      const uint32_t a0 = __byte_perm(x.v[0][w], x.v[1][w], 0x5140);
-      const uint32_t a1 = __byte_perm(x.v[0][w], x.v[1][w], 0x7362);
-      const uint32_t b0 = __byte_perm(x.v[2][w], x.v[3][w], 0x5140);
-      const uint32_t b1 = __byte_perm(x.v[2][w], x.v[3][w], 0x7362);
-      mma_f16(o[4 * w + 0], p, e4m3_lo_f16x2(a0), e4m3_lo_f16x2(b0));
-      mma_f16(o[4 * w + 1], p, e4m3_hi_f16x2(a0), e4m3_hi_f16x2(b0));
-      mma_f16(o[4 * w + 2], p, e4m3_lo_f16x2(a1), e4m3_lo_f16x2(b1));
-      mma_f16(o[4 * w + 3], p, e4m3_hi_f16x2(a1), e4m3_hi_f16x2(b1));
+        for (int n = 0; n < 2; ++n) {
+          const float e0 = ex2_approx(s[2 * b + n][2 * r] - ref[r]);
+          const float e1 = ex2_approx(s[2 * b + n][2 * r + 1] - ref[r]);
+          sum += e0 + e1;
+          p[n * 2 + r] = pack_f16x2(e0, e1);
+        }
+        l[r] = fmaf(sum, vinv, l[r]);
+      }
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) {
+        const uint32_t a0 = __byte_perm(x[b].v[0][w], x[b].v[1][w], 0x5140);
+        const uint32_t a1 = __byte_perm(x[b].v[0][w], x[b].v[1][w], 0x7362);
+        const uint32_t b0 = __byte_perm(x[b].v[2][w], x[b].v[3][w], 0x5140);
+        const uint32_t b1 = __byte_perm(x[b].v[2][w], x[b].v[3][w], 0x7362);
+        mma_f16(o[4 * w + 0], p, e4m3_lo_f16x2(a0), e4m3_lo_f16x2(b0));
+        mma_f16(o[4 * w + 1], p, e4m3_hi_f16x2(a0), e4m3_hi_f16x2(b0));
+        mma_f16(o[4 * w + 2], p, e4m3_lo_f16x2(a1), e4m3_lo_f16x2(b1));
+        mma_f16(o[4 * w + 3], p, e4m3_hi_f16x2(a1), e4m3_hi_f16x2(b1));
+      }
     }
   }
 

@@ -80,7 +80,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);
       mbar_init(&empty[i], kDecWarps);
     }
     *s_abort = 0;
@@ -109,28 +109,44 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   w.init();
   bool ok = true;
   if (warp == kDecWarps) {
-    // ---------------- producer: metadata of 32 blocks at a time, then their tiles
+    // ---------------- producer: 32 blocks at a time, a block's tiles as soon as
+    // its index is known, its scales and valid count behind them (a stage is
+    // full when both its tiles and its metadata are there)
     int issued = 0;
     for (int c0 = 0; ok && c0 < count; c0 += 32) {
-      int blk = e0 + c0 + lane, valid = kBlk;
+      int blk = e0 + c0 + lane;
+      if (a.idx != nullptr && c0 + lane < count) {
+        blk = a.idx[bh * a.n_sel + blk];
+        if (blk < 0 || blk >= a.n_blocks) {
+          report(a.d_err, BSA_DEV_BAD_INDEX);
+          blk = 0;
+        }
+      }
+      int valid = kBlk;
       float ks = 1.f, vs = 1.f;
       if (c0 + lane < count) {
-        if (a.idx != nullptr) {
-          blk = a.idx[bh * a.n_sel + blk];
-          if (blk < 0 || blk >= a.n_blocks) {
-            report(a.d_err, BSA_DEV_BAD_INDEX);
-            blk = 0;
-          }
-        }
         valid = a.block_valid[blk];
-        if (valid < 1 || valid > kBlk) {
-          report(a.d_err, BSA_DEV_BAD_VALID);
-          valid = valid < 1 ? 1 : kBlk;
-        }
-        ks = checked_scale(a.k_scale[bh * a.max_blocks + blk], a.d_err);
-        vs = checked_scale(a.v_scale[bh * a.max_blocks + blk], a.d_err);
+        ks = a.k_scale[bh * a.max_blocks + blk];
+        vs = a.v_scale[bh * a.max_blocks + blk];
       }
-      const float vlog2 = log2f(vs), vinv = 1.f / vs;
+      // The first stages are empty: their copies go out ahead of the loads above.
+      auto copy = [&](int u) {
+        const int st = u % L::kStages;
+        const int row = static_cast<int>((bh * a.max_blocks + blk) * kBlk);
+        uint8_t* dst = sm + L::kRing + st * 2 * L::kTile;
+        mbar_expect_tx(&full[st], 2 * L::kTile);
+        tma_load_2d(dst, &tm_k, 0, row, &full[st]);
+        tma_load_2d(dst + L::kTile, &tm_v, 0, row, &full[st]);
+      };
+      if (c0 == 0 && lane < min(count, L::kStages)) copy(lane);
+      if (valid < 1 || valid > kBlk) {
+        report(a.d_err, BSA_DEV_BAD_VALID);
+        valid = valid < 1 ? 1 : kBlk;
+      }
+      ks = checked_scale(ks, a.d_err);
+      vs = checked_scale(vs, a.d_err);
+      const uint4 meta = make_uint4(__float_as_uint(ks), __float_as_uint(log2f(vs)),
+                                    __float_as_uint(1.f / vs), static_cast<uint32_t>(valid));
       for (int i = 0; ok && i < 32 && c0 + i < count; ++i) {
         const int u = c0 + i, st = u % L::kStages;
         if (u >= L::kStages)
@@ -138,18 +154,15 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
                                                          s_abort, kDecWait));
         if (!ok) break;
         if (lane == i) {
-          float4* meta = reinterpret_cast<float4*>(sm + L::kMeta) + st;
-          *meta = make_float4(ks, vlog2, vinv, __int_as_float(valid));
-          const int row = static_cast<int>((bh * a.max_blocks + blk) * kBlk);
-          uint8_t* dst = sm + L::kRing + st * 2 * L::kTile;
-          mbar_expect_tx(&full[st], 2 * L::kTile);
-          tma_load_2d(dst, &tm_k, 0, row, &full[st]);
-          tma_load_2d(dst + L::kTile, &tm_v, 0, row, &full[st]);
+          reinterpret_cast<uint4*>(sm + L::kMeta)[st] = meta;
+          if (u >= L::kStages) copy(u);
+          mbar_arrive(&full[st]);
         }
         __syncwarp();
         issued = u + 1;
       }
     }
+    if (issued < min(count, L::kStages)) issued = min(count, L::kStages);
     // Copies in flight land before the ring is reused or the CTA exits.
     for (int u = max(0, issued - L::kStages); u < issued; ++u)
       mbar_wait_bounded(&full[u % L::kStages], (u / L::kStages) & 1, nullptr, kDecWait);
@@ -165,11 +178,11 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const uint4 meta = lds128(base + L::kMeta + st * 16);
       const int valid = static_cast<int>(meta.w);
       if (warp * 16 < valid) {
-        typename W::Keys x;
+        typename W::Keys x[1];
         const uint32_t kt = base + L::kRing + st * 2 * L::kTile;
-        w.load_keys(kt, kt + L::kTile, warp * 16, valid, x);
-        w.step(x, warp * 16, valid, __uint_as_float(meta.x), __uint_as_float(meta.y),
-               __uint_as_float(meta.z));
+        w.load_keys(kt, kt + L::kTile, warp * 16, valid, x[0]);
+        const uint4 ms[1] = {meta};
+        w.step(x, warp * 16, ms);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
