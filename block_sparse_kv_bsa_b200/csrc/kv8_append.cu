@@ -63,7 +63,7 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long bN = static_cast<long long>(b) * a.N;
   int va, vb;
-  slot_vectors<MODE>(a.rope.P, slot, va, vb);
+  slot_vectors<D, MODE>(a.rope.P, slot, va, vb);
   SlotTrig g[kRows];
   const uint4* src[kRows];  // the row of head h0; null for a pad row
 #pragma unroll
@@ -83,13 +83,15 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
     }
   };
   load(h0);
+  if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
+    TokenPos pos[kRows];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
-      const int tok = s_tok[row0 + i * kRowStep];
-      slot_trig<MODE>(a.rope, token_pos(a.rope, bN, max(tok, 0)), slot, g[i]);
-      if (tok < 0) g[i].n = 0;  // pad rows stay +0
-    }
+    for (int i = 0; i < kRows; ++i)
+      pos[i] = token_pos(a.rope, bN, max(s_tok[row0 + i * kRowStep], 0));
+    slot_trig<MODE, kRows>(a.rope, pos, slot, va, vb, g);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (s_tok[row0 + i * kRowStep] < 0) g[i].n = 0;  // pad rows stay +0
   }
   for (int h = h0; h < h1; ++h) {
     const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block +
@@ -197,7 +199,7 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
                    (pack_e4m3x2(q[i][4 * e + 2] * mul, q[i][4 * e + 3] * mul) << 16);
       }
       uint8_t* row = dst + (row0 + i * kRowStep) * D;
-      if (MODE == kRopeHalf) {
+      if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
         *reinterpret_cast<uint2*>(row + va * 8) = make_uint2(w[0], w[1]);
         *reinterpret_cast<uint2*>(row + vb * 8) = make_uint2(w[2], w[3]);
       } else {  // the two vectors are neighbours
@@ -220,8 +222,8 @@ append8_kernel(Append8Args a) {
   const int slot0 = j * kBlk;
   const int valid = min(kBlk, a.N - slot0);
   const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
-  invert_block_slots<kApp8Threads>(a.perm, a.N, slot0, s_tok, j == 0 && first_cta, a.d_err, a.T,
-                                   a.H, a.W);
+  find_block_tokens<kApp8Threads>(a.perm, a.N, slot0, valid, s_tok, j == 0 && first_cta, a.d_err,
+                                  a.T, a.H, a.W);
   if (first_cta && threadIdx.x == 0) a.block_valid[a.base_block + j] = valid;
   // A slot of the chunk that no token maps to: perm is not a permutation.
   if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);

@@ -73,13 +73,13 @@ __device__ __forceinline__ uint4 ld_v4(const uint4* p) {
 // vectors).  All of a row's slots are lanes of one warp and the warp has read
 // the rows before it writes any, so src and dst may be the same rows; `on` is
 // false for a lane without a slot.
-template <int MODE>
+template <int D, int MODE>
 __device__ __forceinline__ void turn_heads(const RopeArgs& r, const TokenPos& pos, int slot,
                                            bool on, const uint4* src, long long src_step,
                                            uint4* dst, long long dst_step, int h0, int h1) {
-  SlotTrig g;
+  SlotTrig g[1];
   int va, vb;
-  slot_vectors<MODE>(r.P, slot, va, vb);
+  slot_vectors<D, MODE>(r.P, slot, va, vb);
   if (MODE == kRopeHalfAny) {
     for (int h = h0; h < h1; ++h) {
       float a[8], b[8];
@@ -95,7 +95,10 @@ __device__ __forceinline__ void turn_heads(const RopeArgs& r, const TokenPos& po
     return;
   }
   if (!on) return;
-  if (MODE != kRopeNone) slot_trig<MODE>(r, pos, slot, g);
+  if (MODE != kRopeNone) {
+    const TokenPos at[1] = {pos};
+    slot_trig<MODE, 1>(r, at, slot, va, vb, g);
+  }
   for (int h = h0; h < h1; h += kHeadsInFlight) {
     uint4 x[kHeadsInFlight], y[kHeadsInFlight];
 #pragma unroll
@@ -112,7 +115,7 @@ __device__ __forceinline__ void turn_heads(const RopeArgs& r, const TokenPos& po
         float a[8], b[8];
         unpack8(x[u], a);
         unpack8(y[u], b);
-        turn_slot<MODE>(g, a, b);
+        turn_slot<MODE>(g[0], a, b);
         x[u] = pack8(a);
         y[u] = pack8(b);
       }
@@ -143,7 +146,7 @@ rope_tokens_kernel(RopeTokensArgs a) {
   const long long row = (bN + (on ? tok : 0)) * a.Hh * kVecs;
   const int h0 = blockIdx.y * a.heads;
   const int h1 = min(h0 + a.heads, a.Hh);
-  turn_heads<MODE>(a.rope, pos, slot, on, a.x + row, kVecs, a.y + row, kVecs, h0, h1);
+  turn_heads<D, MODE>(a.rope, pos, slot, on, a.x + row, kVecs, a.y + row, kVecs, h0, h1);
 }
 
 // The chunk's tokens into blocks, K (or the one tensor) turned, V as it is:
@@ -161,12 +164,97 @@ struct RopeBlocksArgs {
   int T, H, W;
 };
 
+constexpr int kBlocksThreads = 512;
+
+// Heads [h0, h1) of the block's rows.  512 threads hold a whole tile (D/16 slots
+// a row, 2 rows a thread, 1 for D = 64), and the tiles of the next two heads
+// are on their way while one is turned and written.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kRopeThreads)
+__device__ __forceinline__ void blocks_heads(const RopeBlocksArgs& a, int which, int b, int h0,
+                                             int h1, const int* s_tok) {
+  constexpr int kSlots = D / 16, kVecs = D / 8;
+  constexpr int kRowStep = kBlocksThreads / kSlots, kRows = kBlk / kRowStep;
+  constexpr int kAhead = 2;
+  const int slot = threadIdx.x % kSlots, row0 = threadIdx.x / kSlots;
+  const long long bN = static_cast<long long>(b) * a.N;
+  const long long dst_step = a.blk_stride * kBlk * kVecs;
+  uint4* dst = a.dst[which] + (static_cast<long long>(b) * a.Hh + h0) * dst_step +
+               (static_cast<long long>(a.base_block + blockIdx.x) * kBlk + row0) * kVecs;
+  int va, vb;
+  slot_vectors<D, MODE>(a.rope.P, slot, va, vb);
+  const uint4* src[kRows];  // the row of head h0; null for a pad row
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int tok = s_tok[row0 + i * kRowStep];
+    src[i] = tok < 0 ? nullptr : a.src[which] + ((bN + tok) * a.Hh + h0) * kVecs;
+  }
+  uint4 x[kAhead][kRows], y[kAhead][kRows];
+  auto load = [&](int h, uint4(&u)[kRows], uint4(&v)[kRows]) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      u[i] = v[i] = make_uint4(0, 0, 0, 0);
+      if (MODE != kRopeHalfAny && h < h1 && src[i] != nullptr) {
+        u[i] = ld_nc_v4(src[i] + (h - h0) * kVecs + va);
+        v[i] = ld_nc_v4(src[i] + (h - h0) * kVecs + vb);
+      }
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) load(h0 + k, x[k], y[k]);
+  SlotTrig g[kRows];
+  if (MODE == kRopeInterleaved || MODE == kRopeHalf) {
+    TokenPos pos[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      pos[i] = token_pos(a.rope, bN, max(s_tok[row0 + i * kRowStep], 0));
+    slot_trig<MODE, kRows>(a.rope, pos, slot, va, vb, g);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (s_tok[row0 + i * kRowStep] < 0) g[i].n = 0;  // pad rows stay +0
+  }
+  for (int h = h0; h < h1; h += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (h + k >= h1) break;
+      uint4 u[kRows], v[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        u[i] = x[k][i];
+        v[i] = y[k][i];
+      }
+      load(h + k + kAhead, x[k], y[k]);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        if (MODE != kRopeNone) {
+          float p[8], q[8];
+          if (MODE == kRopeHalfAny) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = q[e] = 0.f;
+            if (src[i] != nullptr)
+              turn_slot_any(a.rope, token_pos(a.rope, bN, s_tok[row0 + i * kRowStep]), slot,
+                            reinterpret_cast<const __nv_bfloat16*>(src[i] + (h + k - h0) * kVecs),
+                            p, q);
+          } else {
+            unpack8(u[i], p);
+            unpack8(v[i], q);
+            turn_slot<MODE>(g[i], p, q);
+          }
+          u[i] = pack8(p);
+          v[i] = pack8(q);
+        }
+        uint4* row = dst + (h + k - h0) * dst_step + i * (kRowStep * kVecs);
+        st_v4(row + va, u[i]);
+        st_v4(row + vb, v[i]);
+      }
+    }
+  }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kBlocksThreads, 1)
 rope_blocks_kernel(RopeBlocksArgs a) {
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
-  constexpr int kSlots = D / 16, kVecs = D / 8;
   __shared__ int s_tok[kBlk];
   const int j = blockIdx.x;
   const int b = blockIdx.z / a.tensors;
@@ -174,37 +262,18 @@ rope_blocks_kernel(RopeBlocksArgs a) {
   const int slot0 = j * kBlk;
   const int valid = min(kBlk, a.N - slot0);
   const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
-  invert_block_slots<kRopeThreads>(a.perm, a.N, slot0, s_tok, j == 0 && first_cta, a.d_err, a.T,
-                                   a.H, a.W);
+  find_block_tokens<kBlocksThreads>(a.perm, a.N, slot0, valid, s_tok, j == 0 && first_cta,
+                                    a.d_err, a.T, a.H, a.W);
   if (first_cta && a.block_valid != nullptr && threadIdx.x == 0)
     a.block_valid[a.base_block + j] = valid;
   // A slot of the chunk that no token maps to: perm is not a permutation.
   if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
   const int h0 = blockIdx.y * a.heads;
   const int h1 = min(h0 + a.heads, a.Hh);
-  const int slot = threadIdx.x % kSlots;
-  const long long bN = static_cast<long long>(b) * a.N;
-  const long long dst_step = a.blk_stride * kBlk * kVecs;
-  for (int row = threadIdx.x / kSlots; row < kBlk; row += kRopeThreads / kSlots) {
-    const int tok = s_tok[row];
-    uint4* dst = a.dst[which] + static_cast<long long>(b) * a.Hh * dst_step +
-                 (static_cast<long long>(a.base_block + j) * kBlk + row) * kVecs;
-    if (tok < 0) {  // pad row
-      for (int h = h0; h < h1; ++h) {
-        st_v4(dst + h * dst_step + 2 * slot, make_uint4(0, 0, 0, 0));
-        st_v4(dst + h * dst_step + 2 * slot + 1, make_uint4(0, 0, 0, 0));
-      }
-    }
-    const bool on = tok >= 0;
-    const long long src_row = (bN + (on ? tok : 0)) * a.Hh * kVecs;
-    if (which == 0) {
-      const TokenPos pos = token_pos(a.rope, bN, on ? tok : 0);
-      turn_heads<MODE>(a.rope, pos, slot, on, a.src[0] + src_row, kVecs, dst, dst_step, h0, h1);
-    } else {
-      turn_heads<kRopeNone>(a.rope, TokenPos{}, slot, on, a.src[1] + src_row, kVecs, dst,
-                            dst_step, h0, h1);
-    }
-  }
+  if (which == 0)
+    blocks_heads<D, MODE>(a, 0, b, h0, h1, s_tok);
+  else
+    blocks_heads<D, kRopeNone>(a, 1, b, h0, h1, s_tok);
 }
 
 template <int D>
@@ -221,7 +290,7 @@ static bsa_status launch_tokens(int mode, const RopeTokensArgs& a, int B, cudaSt
 template <int D>
 static bsa_status launch_blocks(int mode, const RopeBlocksArgs& a, int B, int nb, cudaStream_t s) {
   dim3 grid(nb, (a.Hh + a.heads - 1) / a.heads, B * a.tensors);
-  const dim3 block(kRopeThreads);
+  const dim3 block(kBlocksThreads);
   if (mode == kRopeInterleaved)
     return launch_pdl(rope_blocks_kernel<D, kRopeInterleaved>, grid, block, 0, s, a);
   if (mode == kRopeHalf) return launch_pdl(rope_blocks_kernel<D, kRopeHalf>, grid, block, 0, s, a);
@@ -328,7 +397,7 @@ extern "C" bsa_status bsa_tokens_to_blocks_rope(const void* x_tok, void* x_blk, 
   a.N = n;
   a.Hh = Hh;
   a.tensors = 1;
-  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh, 2, 2.0);
+  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh, 1, 2.0);
   a.blk_stride = nb;
   a.T = T;
   a.H = H;
@@ -367,7 +436,7 @@ extern "C" bsa_status bsa_kv_append_rope(bsa_kv_cache* c, const void* k_tok, con
   a.N = n;
   a.Hh = c->Hh;
   a.tensors = 2;
-  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 2, 2.0);
+  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 1, 2.0);
   a.blk_stride = c->max_blocks;
   a.base_block = c->n_blocks;
   a.T = T;

@@ -3,9 +3,11 @@
 // A row of D elements is handled in D/16 slots; a thread owns one slot of a
 // row: two 16-byte vectors that hold eight whole pairs (or none), so a pair
 // never crosses threads and a row may be turned in place.
-//   interleaved   slot s: vectors 2s and 2s + 1, pairs 8s .. 8s + 7
+//   interleaved   slot s: vectors s and s + D/16, four pairs in each
 //   half, P % 8 = 0  slot s < P/8: vectors s and s + P/8, pairs 8s .. 8s + 7;
 //                 the vectors past 2P, two a slot, are copied
+// (neighbouring lanes take neighbouring vectors: with the two vectors of a slot
+// side by side every load and store moved half sectors, 6 % of a rope call)
 //   half, any P   the elements of pair i and i + P fall anywhere in their
 //                 vectors: slot s owns elements 16s .. 16s + 15 of the output
 //                 and fetches each element's partner by itself (kHalfAny)
@@ -77,13 +79,25 @@ __device__ __forceinline__ void turn_trig(uint32_t turn, float& c, float& s) {
   c = __uint_as_float(__float_as_uint(v) ^ (((quarter + 1) & 2) << 30));
 }
 
-// cos and sin of pair i (amplitude and direction applied).
-__device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, int i, float& c,
-                                          float& s) {
-  const int ax = i < r.p0 ? 0 : (i < r.p01 ? 1 : 2);
-  const long long p = static_cast<long long>(ax == 0 ? t.p[0] : (ax == 1 ? t.p[1] : t.p[2])) +
-                      (ax == 0 ? r.o0 : (ax == 1 ? r.o1 : r.o2));
-  const uint64_t turn = static_cast<uint64_t>(p) * __ldg(r.phase + i);
+// A pair's frequency and the position it goes by.
+struct PairPhase {
+  uint64_t step;
+  int axis;
+  long long origin;
+};
+__device__ __forceinline__ PairPhase pair_phase(const RopeArgs& r, int i) {
+  PairPhase f;
+  f.step = __ldg(r.phase + i);
+  f.axis = i < r.p0 ? 0 : (i < r.p01 ? 1 : 2);
+  f.origin = f.axis == 0 ? r.o0 : (f.axis == 1 ? r.o1 : r.o2);
+  return f;
+}
+
+// cos and sin of a pair (amplitude and direction applied).
+__device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, const PairPhase& f,
+                                          float& c, float& s) {
+  const int at = f.axis == 0 ? t.p[0] : (f.axis == 1 ? t.p[1] : t.p[2]);
+  const uint64_t turn = static_cast<uint64_t>(at + f.origin) * f.step;
   turn_trig(static_cast<uint32_t>(turn >> 32), c, s);
   c *= r.amp;
   s *= r.inverse ? -r.amp : r.amp;
@@ -92,28 +106,51 @@ __device__ __forceinline__ void pair_trig(const RopeArgs& r, const TokenPos& t, 
 // The eight pairs of a slot; pairs at or past P are left alone.
 struct SlotTrig {
   float c[8], s[8];
-  int n;  // pairs of the slot that are turned, 0..8
+  int n;  // bit e: pair e of the slot is turned (half layout: all or none)
 };
 
+// Pair e of a slot whose vectors are va and vb.
 template <int MODE>
-__device__ __forceinline__ void slot_trig(const RopeArgs& r, const TokenPos& t, int slot,
-                                          SlotTrig& g) {
-  const int n = r.P - slot * 8;
-  g.n = n < 0 ? 0 : (n > 8 ? 8 : n);
+__device__ __forceinline__ int slot_pair(int slot, int va, int vb, int e) {
+  if (MODE == kRopeInterleaved) return e < 4 ? 4 * va + e : 4 * vb + e - 4;
+  return slot * 8 + e;
+}
+
+// The angles of a slot for kRows tokens.
+template <int MODE, int kRows>
+__device__ __forceinline__ void slot_trig(const RopeArgs& r, const TokenPos (&t)[kRows], int slot,
+                                          int va, int vb, SlotTrig (&g)[kRows]) {
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) g[i].n = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    g.c[e] = 1.f;
-    g.s[e] = 0.f;
-    if (e < g.n) pair_trig(r, t, slot * 8 + e, g.c[e], g.s[e]);
+    const int pair = slot_pair<MODE>(slot, va, vb, e);
+    if (pair < r.P) {
+      const PairPhase f = pair_phase(r, pair);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        pair_trig(r, t[i], f, g[i].c[e], g[i].s[e]);
+        g[i].n |= 1 << e;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        g[i].c[e] = 1.f;
+        g[i].s[e] = 0.f;
+      }
+    }
   }
 }
 
-// The two vectors of a slot.
-template <int MODE>
+// The two vectors of a slot of a D-wide row.
+template <int D, int MODE>
 __device__ __forceinline__ void slot_vectors(int P, int slot, int& va, int& vb) {
   if (MODE == kRopeHalf && slot < P / 8) {
     va = slot;
     vb = slot + P / 8;
+  } else if (MODE == kRopeInterleaved) {
+    va = slot;
+    vb = slot + D / 16;
   } else {
     // Half layout: P/8 slots have taken the first P/4 vectors, so the
     // copied ones are again two a slot, at 2s and 2s + 1.
@@ -143,8 +180,8 @@ __device__ __forceinline__ void turn_slot(const SlotTrig& g, float (&a)[8], floa
   if (MODE == kRopeInterleaved) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (e < g.n) turn_pair(a[2 * e], a[2 * e + 1], g.c[e], g.s[e]);
-      if (e + 4 < g.n) turn_pair(b[2 * e], b[2 * e + 1], g.c[e + 4], g.s[e + 4]);
+      if (g.n >> e & 1) turn_pair(a[2 * e], a[2 * e + 1], g.c[e], g.s[e]);
+      if (g.n >> (e + 4) & 1) turn_pair(b[2 * e], b[2 * e + 1], g.c[e + 4], g.s[e + 4]);
     }
   } else if (MODE == kRopeHalf) {
     if (g.n != 0) {
@@ -167,7 +204,7 @@ __device__ __forceinline__ void turn_slot_any(const RopeArgs& r, const TokenPos&
       const int i = second ? el - r.P : el;
       const float w = __bfloat162float(row[second ? i : i + r.P]);
       float c, s;
-      pair_trig(r, t, i, c, s);
+      pair_trig(r, t, pair_phase(r, i), c, s);
       v = second ? w * s + v * c : v * c - w * s;
     }
 #pragma unroll

@@ -91,4 +91,49 @@ __device__ __forceinline__ void invert_block_slots(const int32_t* perm, int N, i
   __syncthreads();
 }
 
+// The same for the kernels that turn tokens: CTAs of NT threads start with it
+// alone on their SM, so it is kept short (per entry one subtraction, one
+// comparison and a predicated store; entries outside [0, N) fall outside the
+// block's `valid` slots, and only the CTA that reports looks at them).
+template <int NT>
+__device__ __forceinline__ void find_block_tokens(const int32_t* perm, int N, int slot0, int valid,
+                                                  int* s_tok, bool report_bad, int32_t* d_err,
+                                                  int T, int H, int W) {
+  static_assert(NT >= kBlk, "one thread per slot clears the table");
+  if (perm == nullptr || (reinterpret_cast<uintptr_t>(perm) & 15u) != 0) {
+    invert_block_slots<NT>(perm, N, slot0, s_tok, report_bad, d_err, T, H, W);
+    return;
+  }
+  if (threadIdx.x < kBlk) s_tok[threadIdx.x] = -1;
+  __syncthreads();
+  const int4* perm4 = reinterpret_cast<const int4*>(perm);
+  auto take = [&](int r, int p) {
+    const unsigned d = static_cast<unsigned>(p - slot0);
+    if (d < static_cast<unsigned>(valid)) s_tok[d] = r;
+  };
+  const int n4 = N / 4;
+  constexpr int kScan = 4;
+  for (int base = threadIdx.x; base < n4; base += kScan * NT) {
+    int4 pv[kScan];
+#pragma unroll
+    for (int k = 0; k < kScan; ++k)
+      pv[k] = base + k * NT < n4 ? __ldg(perm4 + base + k * NT) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int k = 0; k < kScan; ++k) {
+      const int r = 4 * (base + k * NT);
+      take(r, pv[k].x);
+      take(r + 1, pv[k].y);
+      take(r + 2, pv[k].z);
+      take(r + 3, pv[k].w);
+    }
+  }
+  for (int r = 4 * n4 + threadIdx.x; r < N; r += NT) take(r, __ldg(perm + r));
+  if (report_bad) {
+    for (int r = threadIdx.x; r < N; r += NT)
+      if (static_cast<unsigned>(__ldg(perm + r)) >= static_cast<unsigned>(N))
+        report(d_err, BSA_DEV_BAD_PERM);
+  }
+  __syncthreads();
+}
+
 }  // namespace bsa
