@@ -1,8 +1,8 @@
 // kv8_decode.cu - bsa_kv8_attn_decode: a few query tokens over the 8-bit
 // cache.
 //
-// The rows of one cache head are its n_tok * group query rows, 16 to a tile
-// (mma.sync, attn8_warp.cuh).  With so few rows the call is bound by reading
+// The rows of one cache head are its n_tok * group query rows, 16 to a tile, or
+// one tile of up to 8 (mma.sync, attn8_warp.cuh).  With so few rows the call is bound by reading
 // the cache once (1 byte an element of K and V), so the blocks are split over
 // the SMs and each CTA streams its share through a ring of K and V tiles that
 // TMA keeps full (192 KB: the 50 KB or so that an SM must have in flight to
@@ -64,12 +64,12 @@ __device__ __forceinline__ long long query_row(const Decode8Args& a, long long b
   return (b * a.n_tok + r / a.group) * a.Hq + h * a.group + r % a.group;
 }
 
-template <int D>
+// W is AttnWarp16<D>, or AttnWarp8<D> for at most 8 rows in all.
+template <int D, class W>
 __global__ void __launch_bounds__(kDecThreads, 1)
 decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                Decode8Args a) {
   using L = DecodeLayout<D>;
-  using W = AttnWarp<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~static_cast<uintptr_t>(1023));
@@ -77,7 +77,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBars);
   uint64_t* empty = full + L::kStages;
   volatile int* s_abort = reinterpret_cast<volatile int*>(sm + L::kMisc);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(&full[i], 2);
@@ -106,7 +106,6 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int e0 = min(n, split * per), count = min(n - e0, per);
 
   W w;
-  w.init();
   bool ok = true;
   if (warp == kDecWarps) {
     // ---------------- producer: 32 blocks at a time, a block's tiles as soon as
@@ -167,9 +166,12 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int u = max(0, issued - L::kStages); u < issued; ++u)
       mbar_wait_bounded(&full[u % L::kStages], (u / L::kStages) & 1, nullptr, kDecWait);
   } else {
-    const int r0 = tile * 16 + g;
-    w.load_q(r0 < a.rows ? a.q + query_row(a, bh, r0) * D : nullptr,
-             r0 + 8 < a.rows ? a.q + query_row(a, bh, r0 + 8) * D : nullptr, a.scale_log2);
+    w.init(
+        [&](int r) {
+          r += tile * 16;
+          return r < a.rows ? a.q + query_row(a, bh, r) * D : nullptr;
+        },
+        a.scale_log2);
     for (int u = 0; ok && u < count; ++u) {
       const int st = u % L::kStages;
       ok = __all_sync(0xffffffffu,
@@ -178,16 +180,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const uint4 meta = lds128(base + L::kMeta + st * 16);
       const int valid = static_cast<int>(meta.w);
       if (warp * 16 < valid) {
-        typename W::Keys x[1];
+        typename W::Keys x;
         const uint32_t kt = base + L::kRing + st * 2 * L::kTile;
-        w.load_keys(kt, kt + L::kTile, warp * 16, valid, x[0]);
-        const uint4 ms[1] = {meta};
-        w.step(x, warp * 16, ms);
+        W::Tile::load_keys(kt, kt + L::kTile, warp * 16, valid, x);
+        w.step(x, warp * 16, meta);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }
-    w.finish();
   }
   if (!ok && lane == 0) {
     report(a.d_err, BSA_DEV_WAIT_TIMEOUT);
@@ -198,21 +198,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   __syncthreads();
   float* s_o = reinterpret_cast<float*>(sm + L::kOut);  // [warp][16][D]
   float* s_ml = reinterpret_cast<float*>(sm + L::kMl);  // [warp][16][2]
-  if (warp < kDecWarps) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float* o = s_o + (warp * 16 + g + 8 * r) * D;
-#pragma unroll
-      for (int i = 0; i < W::kTiles; ++i) {
-        o[(2 * t) * (D / 8) + i] = w.o[i][2 * r];
-        o[(2 * t + 1) * (D / 8) + i] = w.o[i][2 * r + 1];
-      }
-      if (t == 0) {
-        s_ml[(warp * 16 + g + 8 * r) * 2] = w.m[r];
-        s_ml[(warp * 16 + g + 8 * r) * 2 + 1] = w.l[r];
-      }
-    }
-  }
+  if (warp < kDecWarps) w.finish(s_o + warp * 16 * D, s_ml + warp * 32);
   __syncthreads();
   const int rows = min(16, a.rows - tile * 16);
   for (int i = threadIdx.x; i < rows * D; i += kDecThreads) {
@@ -356,11 +342,15 @@ static bsa_status launch_decode(const Decode8Args& a, const bsa_kv_cache8* c, cu
   const long long crows = bh * c->max_blocks * kBlk;
   if (!make_map8(&tk, c->k, crows, D) || !make_map8(&tv, c->v, crows, D)) return BSA_ERR_CUDA;
   const int smem = DecodeLayout<D>::kAlloc;
-  if (cudaFuncSetAttribute(decode8_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-      cudaSuccess)
-    return BSA_ERR_CUDA;
-  BSA_TRY(launch_pdl(decode8_kernel<D>, dim3(static_cast<unsigned>(bh * a.tiles), a.n_split),
-                     dim3(kDecThreads), static_cast<size_t>(smem), s, tk, tv, a));
+  auto go = [&](void (*kernel)(const CUtensorMap, const CUtensorMap, Decode8Args)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
+      return BSA_ERR_CUDA;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(bh * a.tiles), a.n_split),
+                      dim3(kDecThreads), static_cast<size_t>(smem), s, tk, tv, a);
+  };
+  BSA_TRY(a.rows <= AttnWarp8<D>::kRows ? go(decode8_kernel<D, AttnWarp8<D>>)
+                                        : go(decode8_kernel<D, AttnWarp16<D>>));
   if (a.n_split == 1) return BSA_OK;
   return launch_pdl(decode8_join_kernel<D>, dim3(static_cast<unsigned>(bh), a.rows),
                     dim3(kJoinThreads), 0, s, a);
