@@ -210,6 +210,12 @@ __device__ __forceinline__ float move_reference(float mx, float& m, float& l) {
   return fix;
 }
 
+// Element of a row at column c of what finish() writes.
+template <int D>
+__device__ __forceinline__ int out_element(int c) {
+  return (c & 7) * (D / 8) + (c >> 3);
+}
+
 // 16 query rows: lane (g, t) has rows g and g + 8.
 template <int D>
 struct AttnWarp16 {
@@ -314,7 +320,11 @@ struct AttnWarp16 {
     }
   }
 
-  // Sums over the lanes of a row; O [16][D] and (m, l) [16][2] to shared memory.
+  // Sums over the lanes of a row; O [16][kStride] and (m, l) [16][2] to shared
+  // memory.  Element d = n * (D / 8) + i of a row goes to column i * 8 + n
+  // (out_element is the way back), and rows are kStride apart: lanes then write
+  // different banks, where d as it is would put all 32 into one.
+  static constexpr int kStride = D + 8;
   __device__ __forceinline__ void finish(float* s_o, float* s_ml) {
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
 #pragma unroll
@@ -324,8 +334,8 @@ struct AttnWarp16 {
       const int row = g + 8 * r;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
-        s_o[row * D + (2 * t) * (D / 8) + i] = o[i][2 * r];
-        s_o[row * D + (2 * t + 1) * (D / 8) + i] = o[i][2 * r + 1];
+        *reinterpret_cast<float2*>(s_o + row * kStride + i * 8 + 2 * t) =
+            make_float2(o[i][2 * r], o[i][2 * r + 1]);
       }
       if (t == 0) {
         s_ml[row * 2] = m[r];
@@ -433,6 +443,7 @@ struct AttnWarp8 {
     }
   }
 
+  static constexpr int kStride = D + 4;
   __device__ __forceinline__ void finish(float* s_o, float* s_ml) {
     const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
 #pragma unroll
@@ -442,8 +453,8 @@ struct AttnWarp8 {
       const int row = 2 * t + r;
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
-        s_o[row * D + g * (D / 8) + 2 * i] = o[i][r];
-        s_o[row * D + g * (D / 8) + 2 * i + 1] = o[i][2 + r];
+        s_o[row * kStride + 16 * i + g] = o[i][r];
+        s_o[row * kStride + 16 * i + 8 + g] = o[i][2 + r];
       }
       if (g == 0) {
         s_ml[row * 2] = m[r];

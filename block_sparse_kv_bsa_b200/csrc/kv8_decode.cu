@@ -34,8 +34,8 @@ struct DecodeLayout {
   static constexpr int kMl = kMeta + kStages * 16;             // float [warps][16][2]
   static constexpr int kMisc = kMl + kDecWarps * 16 * 8;
   static constexpr int kAlloc = kMisc + 16 + 1024;
-  static constexpr int kOut = kRing;                           // float [warps][16][D] at the end
-  static_assert(kDecWarps * 16 * D * 4 <= kStages * 2 * kTile, "warps' O fits the ring");
+  static constexpr int kOut = kRing;                           // float [warps][16][D + 8] at the end
+  static_assert(kDecWarps * 16 * (D + 8) * 4 <= kStages * 2 * kTile, "warps' O fits the ring");
   static_assert(kAlloc <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -48,7 +48,7 @@ struct Decode8Args {
   const int32_t* cnt;
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;   // [B*Hh*tiles][n_split][16][D]
+  float* part_o;   // [B*Hh*tiles][n_split][16][D], columns as the warps leave them
   float* part_ml;  // [B*Hh*tiles][n_split][16][2]
   int32_t* d_err;
   int Hq, Hh, group, n_tok, rows, tiles, n_split;
@@ -196,13 +196,14 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
 
   // Join the warps: the ring is empty (every tile issued has been read).
   __syncthreads();
-  float* s_o = reinterpret_cast<float*>(sm + L::kOut);  // [warp][16][D]
+  constexpr int kStride = W::kStride;
+  float* s_o = reinterpret_cast<float*>(sm + L::kOut);  // [warp][16][kStride]
   float* s_ml = reinterpret_cast<float*>(sm + L::kMl);  // [warp][16][2]
-  if (warp < kDecWarps) w.finish(s_o + warp * 16 * D, s_ml + warp * 32);
+  if (warp < kDecWarps) w.finish(s_o + warp * 16 * kStride, s_ml + warp * 32);
   __syncthreads();
   const int rows = min(16, a.rows - tile * 16);
   for (int i = threadIdx.x; i < rows * D; i += kDecThreads) {
-    const int r = i / D, d = i % D;
+    const int r = i / D, c = i % D;  // column c as finish() left it
     float m = -INFINITY;
 #pragma unroll
     for (int k = 0; k < kDecWarps; ++k) m = fmaxf(m, s_ml[(k * 16 + r) * 2]);
@@ -212,17 +213,17 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       const float mk = s_ml[(k * 16 + r) * 2];
       const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - m);
       l = fmaf(s_ml[(k * 16 + r) * 2 + 1], f, l);
-      o = fmaf(s_o[(k * 16 + r) * D + d], f, o);
+      o = fmaf(s_o[(k * 16 + r) * kStride + c], f, o);
     }
     if (a.n_split == 1) {
       const bool have = m > -INFINITY;
       const long long out = query_row(a, bh, tile * 16 + r);
-      a.o[out * D + d] = __float2bfloat16(have ? o / l : 0.f);
-      if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      a.o[out * D + out_element<D>(c)] = __float2bfloat16(have ? o / l : 0.f);
+      if (c == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else {
       const long long p = (item * a.n_split + split) * 16 + r;
-      a.part_o[p * D + d] = o;
-      if (d == 0) {
+      a.part_o[p * D + c] = o;
+      if (c == 0) {
         a.part_ml[p * 2] = m;
         a.part_ml[p * 2 + 1] = l;
       }
@@ -281,7 +282,7 @@ decode8_join_kernel(Decode8Args a) {
   for (int k = 1; k < kGroups; ++k) acc += s_acc[k * D + d];
   const bool have = m > -INFINITY;
   const long long out = query_row(a, bh, row);
-  a.o[out * D + d] = __float2bfloat16(have ? acc / l : 0.f);
+  a.o[out * D + out_element<D>(d)] = __float2bfloat16(have ? acc / l : 0.f);
   if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
