@@ -21,7 +21,6 @@ constexpr int kDecWarps = 8;                          // consumers: 16 keys of e
 constexpr int kDecThreads = kDecWarps * 32 + 32;      // and one producer warp
 constexpr int kDecSlots = 148;     // CTAs resident at once: one on each SM
 constexpr int kDecMaxRows = 128;   // query rows of one cache head
-constexpr int kDecMaxSplit = 148;
 constexpr long long kDecWait = 1LL << 31;  // SM clocks (about a second)
 
 template <int D>
@@ -95,6 +94,10 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   const int tile = static_cast<int>(item % a.tiles);
 
   int n = a.n_sel;
+  const int guess0 = min(n, split * ((n + a.n_split - 1) / a.n_split));
+  int guess = -1;
+  if (warp == kDecWarps && a.idx != nullptr && guess0 + lane < n)
+    guess = a.idx[bh * a.n_sel + guess0 + lane];
   if (a.cnt != nullptr) {
     n = a.cnt[bh];
     if (n < 0 || n > a.n_sel) {
@@ -115,7 +118,9 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
     for (int c0 = 0; ok && c0 < count; c0 += 32) {
       int blk = e0 + c0 + lane;
       if (a.idx != nullptr && c0 + lane < count) {
-        blk = a.idx[bh * a.n_sel + blk];
+        // The first entries were read beside the count, where a full route
+        // has them.
+        blk = c0 == 0 && e0 == guess0 ? guess : a.idx[bh * a.n_sel + blk];
         if (blk < 0 || blk >= a.n_blocks) {
           report(a.d_err, BSA_DEV_BAD_INDEX);
           blk = 0;
@@ -231,59 +236,62 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
   }
 }
 
-// Joins the splits of one query row.
-constexpr int kJoinThreads = 256;
+// Joins the splits of one query row: warp w takes splits w, w + 8, ..., each
+// lane D / 32 columns; every warp works out the common maximum and sum for
+// itself, so the parts are on their way from the start and one barrier joins
+// the warps.
+constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 decode8_join_kernel(Decode8Args a) {
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
-  __shared__ float s_w[kDecMaxSplit];
-  __shared__ float s_red[2][kJoinThreads / 32];
-  __shared__ float s_acc[kJoinThreads];
+  constexpr int kCols = D / 32;
+  __shared__ float s_acc[kJoinWarps][D];
   const int row = blockIdx.y;
   const long long bh = blockIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const long long p0 = (bh * a.tiles + row / 16) * a.n_split * 16 + row % 16;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + p0;
+  const float* part = a.part_o + p0 * D + lane * kCols;
+  float v[kCols], acc[kCols];
+  auto load = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) v[c] = s < a.n_split ? part[s * (16 * D) + c] : 0.f;
+  };
+  load(warp);
   float m = -INFINITY;
-  for (int s = threadIdx.x; s < a.n_split; s += kJoinThreads)
-    m = fmaxf(m, a.part_ml[(p0 + s * 16) * 2]);
+  for (int s = lane; s < a.n_split; s += 32) m = fmaxf(m, ml[s * 16].x);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) s_red[0][warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) m = fmaxf(m, s_red[0][k]);
   float l = 0.f;
-  for (int s = threadIdx.x; s < a.n_split; s += kJoinThreads) {
-    const float ms = a.part_ml[(p0 + s * 16) * 2];
-    const float f = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
-    s_w[s] = f;
-    l = fmaf(a.part_ml[(p0 + s * 16) * 2 + 1], f, l);
+  for (int s = lane; s < a.n_split; s += 32) {
+    const float2 x = ml[s * 16];
+    l = fmaf(x.y, x.x == -INFINITY ? 0.f : ex2_approx(x.x - m), l);
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-  if (lane == 0) s_red[1][warp] = l;
-  __syncthreads();
-  l = 0.f;
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) l += s_red[1][k];
-  constexpr int kGroups = kJoinThreads / D;
-  const int d = threadIdx.x % D, grp = threadIdx.x / D;
-  float acc = 0.f;
-#pragma unroll 8
-  for (int s = grp; s < a.n_split; s += kGroups)
-    acc = fmaf(a.part_o[(p0 + s * 16) * D + d], s_w[s], acc);
-  s_acc[threadIdx.x] = acc;
-  __syncthreads();
-  if (grp != 0) return;
+  for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
+  for (int s = warp; s < a.n_split; s += kJoinWarps) {
+    const float ms = ml[s * 16].x;
+    const float f = ms == -INFINITY ? 0.f : ex2_approx(ms - m);
 #pragma unroll
-  for (int k = 1; k < kGroups; ++k) acc += s_acc[k * D + d];
+    for (int c = 0; c < kCols; ++c) acc[c] = fmaf(v[c], f, acc[c]);
+    load(s + kJoinWarps);
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) s_acc[warp][lane * kCols + c] = acc[c];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float o = 0.f;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) o += s_acc[w][threadIdx.x];
   const bool have = m > -INFINITY;
   const long long out = query_row(a, bh, row);
-  a.o[out * D + out_element<D>(d)] = __float2bfloat16(have ? acc / l : 0.f);
-  if (d == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  a.o[out * D + out_element<D>(threadIdx.x)] = __float2bfloat16(have ? o / l : 0.f);
+  if (threadIdx.x == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 // Splits of n_sel blocks: the count whose waves over the resident CTAs leave
@@ -354,7 +362,7 @@ static bsa_status launch_decode(const Decode8Args& a, const bsa_kv_cache8* c, cu
                                         : go(decode8_kernel<D, AttnWarp16<D>>));
   if (a.n_split == 1) return BSA_OK;
   return launch_pdl(decode8_join_kernel<D>, dim3(static_cast<unsigned>(bh), a.rows),
-                    dim3(kJoinThreads), 0, s, a);
+                    dim3(kJoinWarps * 32), 0, s, a);
 }
 
 }  // namespace bsa
