@@ -571,7 +571,8 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       uint4 meta = make_uint4(__float_as_uint(1.f), 0, __float_as_uint(1.f), kBlk);
       if (ok) meta = lds_v4(smem_u32(sm + L::kMeta) + (t % (2 * kMetaTiles)) * 16);
       if (t % kMetaTiles == kMetaTiles - 2 + g) mbar_arrive(&bars[A_META_EMPTY + meta_half(t)]);
-      const float factor = row_scale * __uint_as_float(meta.x);
+      // Never zero (sm_scale = 0, or underflow): a masked key's -inf stays -inf.
+      const float factor = fmaxf(row_scale * __uint_as_float(meta.x), 1.1754944e-38f);
       const float vlog2 = __uint_as_float(meta.y), vinv = __uint_as_float(meta.z);
       const int valid = static_cast<int>(meta.w);
       const uint32_t s_col = static_cast<uint32_t>(t % kS8Bufs) * 128;

@@ -299,7 +299,7 @@ decode8_join_kernel(Decode8Args a) {
 // join count as two blocks), fewest first.
 static int most_splits(long long items, int n_sel) {
   long long most = kDecSlots / items;
-  if (most < 8) most = 8;
+  if (most < 8) most = items <= 4 * kDecSlots ? 8 : 1;  // many items fill the SMs as they are
   return static_cast<int>(most < n_sel ? most : n_sel);
 }
 
@@ -390,6 +390,7 @@ extern "C" bsa_status bsa_kv8_attn_decode(const void* q_tok, const bsa_kv_cache8
   if (c->B <= 0 || c->Hh <= 0 || c->max_blocks <= 0 || c->n_blocks < 0 ||
       c->n_blocks > c->max_blocks || (idx != nullptr && max_sel <= 0) || !(sm_scale == sm_scale))
     return BSA_ERR_INVALID_ARG;
+  if (idx != nullptr && max_sel > (1 << 30)) return BSA_ERR_SHAPE;
   if (!aligned16(q_tok) || !aligned16(c->k) || !aligned16(c->v) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return BSA_ERR_INVALID_ARG;

@@ -18,13 +18,12 @@ static __device__ __noinline__ int curve_token_call(int T, int H, int W, int p) 
 }
 
 // Slot -> token for the 128 curve slots [slot0, slot0 + 128) of one block:
-// s_tok[d] is the raster token whose perm entry is slot0 + d, or -1.  The
-// CTA's NT threads (NT >= 128) scan perm in rounds of kScan independent loads
-// per thread (one L2 round trip per round); entries outside [0, N) are
-// skipped, and reported when `report_bad`.  Ends with a CTA barrier.
-// s_tok[d] = the token at curve slot slot0 + d (d < 128), or -1 for a pad
-// slot.  With a table, the CTA scans perm (token -> slot); without one
-// (perm == NULL), each thread locates its slot on the curve.
+// s_tok[d] is the raster token whose perm entry is slot0 + d, or -1 for a pad
+// slot.  With a table, the CTA's NT threads (NT >= 128) scan perm in rounds of
+// kScan independent loads per thread (one L2 round trip per round); entries
+// outside [0, N) are skipped, and reported when `report_bad`.  Without one
+// (perm == NULL), each thread locates its slot on the curve.  Ends with a CTA
+// barrier.
 template <int NT>
 __device__ __forceinline__ void invert_block_slots(const int32_t* perm, int N, int slot0,
                                                    int* s_tok, bool report_bad, int32_t* d_err,

@@ -179,7 +179,7 @@ def check_blocks(q, cache, idx, cnt, o, lse, q_valid, scale):
 @pytest.mark.parametrize("B,Hh,G,D,nqb,blocks,counts", [
     (1, 1, 1, 64, 1, 1, [1]), (1, 2, 1, 64, 2, 5, [1, 2, 3, 5]), (2, 3, 2, 128, 3, 9, [9, 0, 4, 1]),
     (1, 2, 3, 64, 2, 7, [7, 6]), (1, 1, 5, 128, 1, 12, [12]), (2, 1, 1, 128, 4, 17, [2, 3, 16, 17]),
-    (1, 1, 1, 128, 2, 40, [39, 40])])
+    (1, 1, 1, 128, 2, 40, [39, 40]), (1, 1, 2, 64, 3, 131, [131, 64, 97])])
 def test_attn8(B, Hh, G, D, nqb, blocks, counts):
     rng = np.random.default_rng(7)
     valid = rng.integers(1, 129, size=blocks)
@@ -194,6 +194,49 @@ def test_attn8(B, Hh, G, D, nqb, blocks, counts):
         o, lse = bsa.bsa_kv8_attn(q, cache, idx, cnt, q_valid=qv)
         bsa.raise_on_device_error(DEV)
         check_blocks(q, cache, idx, cnt, o, lse, qv, ref.sm(D))
+
+
+def test_attn8_negative_and_zero_scale():
+    cache = ref.fill_cache(bsa, 1, 1, 64, 3, [128, 128, 50], 15)
+    q = tokens(1, 1, 128, 64, 16).contiguous()
+    idx = torch.arange(3, dtype=torch.int32, device=DEV).view(1, 1, 1, 3)
+    cnt = torch.full((1, 1, 1), 3, dtype=torch.int32, device=DEV)
+    keys, vals = ref.gather(cache, 0, 0, range(3))
+    for scale in (-0.2, 0.0):
+        o, lse = bsa.bsa_kv8_attn(q, cache, idx, cnt, sm_scale=scale)
+        od, ld = bsa.bsa_kv8_attn_decode(q[:, :, :4].transpose(1, 2).contiguous(), cache,
+                                         sm_scale=scale)
+        want = ref.attend(ref.f64(q[0, 0]), keys, vals, scale)
+        ref.check_attn(o[0, 0], lse[0, 0], *want)
+        ref.check_attn(od[0, :, 0], ld[0, :, 0], *(x[:4] for x in want))
+
+
+def test_calls_on_two_streams_at_once():
+    # Two decodes and two appends in flight together, each with what it needs of
+    # its own, give what they give alone.
+    caches = [ref.fill_cache(bsa, 1, 4, 128, 60, [128] * 60, 17 + i) for i in range(2)]
+    qs = [tokens(1, 1, 4, 128, 27 + i) for i in range(2)]
+    ks = [tokens(1, 500, 4, 128, 37 + i) for i in range(2)]
+    _, rope = make((64,), "half")
+
+    def work(i):
+        o, lse = bsa.bsa_kv8_attn_decode(qs[i], caches[i])
+        c = bsa.KVCache8(1, 4, 128, 4, device=DEV)
+        bsa.bsa_kv8_append(c, ks[i], ks[i], 500, 1, 1, rope=rope, origin=(i, 0, 0))
+        return o, lse, c.k.view(torch.uint8), c.k_scale, c.v.view(torch.uint8)
+
+    want = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(work(i))
+        torch.cuda.synchronize()
+        for x, y in zip(got[0] + got[1], want[0] + want[1]):
+            assert torch.equal(x, y)
+    bsa.raise_on_device_error(DEV)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -293,6 +336,12 @@ def test_attn8_gives_the_same_bits_every_time():
         if want is None:
             want = got
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for n_tok in (1, 12):
+        qt = q[:, :, :n_tok].transpose(1, 2).contiguous()
+        want = bsa.bsa_kv8_attn_decode(qt, cache)
+        for _ in range(30):
+            got = bsa.bsa_kv8_attn_decode(qt, cache)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 @pytest.mark.parametrize("what,code", [("index", 1), ("count", 2), ("valid", 3), ("scale", 6),
@@ -327,7 +376,9 @@ def test_attn8_reports_what_only_the_device_sees(what, code):
 @pytest.mark.parametrize("B,Hh,G,D,n_tok,blocks,tail", [
     (1, 1, 1, 64, 1, 1, 1), (1, 2, 1, 64, 1, 10, 128), (2, 3, 4, 128, 1, 33, 77),
     (1, 2, 5, 128, 3, 9, 15), (1, 1, 8, 64, 16, 20, 128), (3, 1, 1, 128, 1, 300, 31),
-    (1, 2, 1, 64, 17, 5, 16), (1, 40, 1, 128, 2, 18, 17)])
+    (1, 2, 1, 64, 17, 5, 16), (1, 40, 1, 128, 2, 18, 17), (1, 1, 8, 128, 1, 150, 100),
+    (1, 2, 8, 64, 1, 4, 1), (1, 1, 16, 128, 1, 3, 127), (2, 1, 9, 128, 1, 30, 2),
+    (2, 90, 1, 64, 1, 41, 65), (7, 90, 2, 64, 1, 33, 128)])
 def test_decode8(B, Hh, G, D, n_tok, blocks, tail):
     valid = [128] * blocks
     valid[-1] = tail
