@@ -32,7 +32,8 @@ struct Append8Args {
   const int32_t* perm;
   int32_t* block_valid;
   int32_t* d_err;
-  int N, Hh, heads;
+  int N, Hh, nb, B;
+  HeadRuns runs;
   int max_blocks, base_block;
   int T, H, W;
 };
@@ -55,9 +56,9 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int D, int MODE, bool kMean>
-__device__ __forceinline__ void append8_heads(const Append8Args& a, int which, int b, int h0,
-                                              int h1, const int* s_tok, int valid, float* s_red,
-                                              float* s_sum) {
+__device__ __forceinline__ void append8_heads(const Append8Args& a, int which, int b, int j,
+                                              int h0, int h1, const int* s_tok, int valid,
+                                              float* s_red, float* s_sum) {
   constexpr int kSlots = D / 16, kVecs = D / 8;
   constexpr int kRowStep = kApp8Threads / kSlots;
   constexpr int kRows = kBlk / kRowStep;  // rows per thread: 2, or 1 for D = 64
@@ -97,8 +98,7 @@ __device__ __forceinline__ void append8_heads(const Append8Args& a, int which, i
       if (s_tok[row0 + i * kRowStep] < 0) g[i].n = 0;  // pad rows stay +0
   }
   for (int h = h0; h < h1; ++h) {
-    const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block +
-                          blockIdx.x;
+    const long long blk = (static_cast<long long>(b) * a.Hh + h) * a.max_blocks + a.base_block + j;
     float p[kRows][8], q[kRows][8];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -220,31 +220,32 @@ append8_kernel(Append8Args a) {
   __shared__ int s_tok[kBlk];
   __shared__ __align__(16) float s_red[2 * kApp8Warps];
   __shared__ float s_sum[2 * kApp8Warps * D];
-  const int j = blockIdx.x;
-  const int b = blockIdx.z / 2, which = blockIdx.z % 2;
-  const int slot0 = j * kBlk;
+  const RunAt at(a.runs, a.nb, a.B, a.Hh);
+  const int slot0 = at.j * kBlk;
   const int valid = min(kBlk, a.N - slot0);
-  const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
-  find_block_tokens<kApp8Threads>(a.perm, a.N, slot0, valid, s_tok, j == 0 && first_cta, a.d_err,
+  find_block_tokens<kApp8Threads>(a.perm, a.N, slot0, valid, s_tok, at.j == 0 && at.first, a.d_err,
                                   a.T, a.H, a.W);
-  if (first_cta && threadIdx.x == 0) a.block_valid[a.base_block + j] = valid;
+  if (at.first && threadIdx.x == 0) a.block_valid[a.base_block + at.j] = valid;
   // A slot of the chunk that no token maps to: perm is not a permutation.
-  if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
-  const int h0 = blockIdx.y * a.heads;
-  const int h1 = min(h0 + a.heads, a.Hh);
-  if (which == 1) {
-    append8_heads<D, kRopeNone, false>(a, 1, b, h0, h1, s_tok, valid, s_red, s_sum);
+  if (at.first && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
+  if (at.which == 1) {
+    append8_heads<D, kRopeNone, false>(a, 1, at.b, at.j, at.h0, at.h1, s_tok, valid, s_red, s_sum);
   } else if (a.kmean != nullptr) {
-    append8_heads<D, MODE, true>(a, 0, b, h0, h1, s_tok, valid, s_red, s_sum);
+    append8_heads<D, MODE, true>(a, 0, at.b, at.j, at.h0, at.h1, s_tok, valid, s_red, s_sum);
   } else {
-    append8_heads<D, MODE, false>(a, 0, b, h0, h1, s_tok, valid, s_red, s_sum);
+    append8_heads<D, MODE, false>(a, 0, at.b, at.j, at.h0, at.h1, s_tok, valid, s_red, s_sum);
   }
 }
 
 template <int D>
-static bsa_status launch_append8(int mode, const Append8Args& a, int B, int nb, cudaStream_t s) {
-  dim3 grid(nb, (a.Hh + a.heads - 1) / a.heads, 2 * B);
-  const dim3 block(kApp8Threads);
+static bsa_status launch_append8(int mode, Append8Args a, cudaStream_t s) {
+  const long long blocks = static_cast<long long>(a.nb) * a.B;
+  // K's and V's tiles cost about the same here (both are reduced and rounded):
+  // runs of one length, a start counting as one head (8 and 8 heads measured
+  // 26.5 us where 12 and 4, which suit rope_blocks_kernel's cost, took 27.6).
+  const int heads = heads_per_cta(2 * blocks, a.Hh, 1, 1.0);
+  a.runs = HeadRuns{{heads, heads}};
+  const dim3 grid(run_ctas(a.runs, blocks, a.Hh, 2)), block(kApp8Threads);
   switch (mode) {
     case kRopeNone: return launch_pdl(append8_kernel<D, kRopeNone>, grid, block, 0, s, a);
     case kRopeInterleaved:
@@ -290,17 +291,15 @@ extern "C" bsa_status bsa_kv8_append(bsa_kv_cache8* c, const void* k_tok, const 
   a.d_err = d_err;
   a.N = n;
   a.Hh = c->Hh;
-  // One CTA to an SM; its start and angles cost about one head's tile
-  // (2500 SM cycles against 2000).
-  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 1, 1.0);
+  a.nb = nb;
+  a.B = c->B;
   a.max_blocks = c->max_blocks;
   a.base_block = c->n_blocks;
   a.T = T;
   a.H = H;
   a.W = W;
   cudaStream_t s = as_stream(stream);
-  BSA_TRY(c->D == 128 ? launch_append8<128>(mode, a, c->B, nb, s)
-                      : launch_append8<64>(mode, a, c->B, nb, s));
+  BSA_TRY(c->D == 128 ? launch_append8<128>(mode, a, s) : launch_append8<64>(mode, a, s));
   c->n_blocks += nb;
   return BSA_OK;
 }

@@ -9,9 +9,10 @@
 // and no table goes through memory.
 //   tokens  40001 x 24 heads x 64, 48 of 64 dimensions: 44.5 us, 5.5 TB/s
 //           (runs of 12 heads; runs of 24, one wave and a half of CTAs: 57 us)
-//   blocks  K and V of 7800 x 24 heads x 128: 38.8 us, 4.9 TB/s.  A CTA's start
+//   blocks  K and V of 7800 x 24 heads x 128: 36 us, 5.3 TB/s.  A CTA's start
 //           (its tokens, angles and first tiles) costs about 3 us, a head's
-//           tile 1.4 us, so runs are long: 24 heads a CTA 39 us, 8 heads 47 us.
+//           tile 1.4 us, so K's runs are long (24 heads) and V's shorter ones
+//           (6) fill the SMs they leave: 24 heads for both took 39 us, 8 47 us.
 #include <math.h>
 
 #include "common.cuh"
@@ -147,7 +148,7 @@ rope_tokens_kernel(RopeTokensArgs a) {
 }
 
 // The chunk's tokens into blocks, K (or the one tensor) turned, V as it is:
-// one CTA per (chunk block, group of heads, batch and tensor).
+// one CTA per block and run of heads of one tensor.
 struct RopeBlocksArgs {
   RopeArgs rope;
   const uint4* src[2];
@@ -155,7 +156,8 @@ struct RopeBlocksArgs {
   const int32_t* perm;
   int32_t* block_valid;  // optional
   int32_t* d_err;
-  int N, Hh, heads, tensors;
+  int N, Hh, nb, B, tensors;
+  HeadRuns runs;
   long long blk_stride;
   int base_block;
   int T, H, W;
@@ -167,8 +169,8 @@ constexpr int kBlocksThreads = 512;
 // a row, 2 rows a thread, 1 for D = 64), and the tiles of the next two heads
 // are on their way while one is turned and written.
 template <int D, int MODE>
-__device__ __forceinline__ void blocks_heads(const RopeBlocksArgs& a, int which, int b, int h0,
-                                             int h1, const int* s_tok) {
+__device__ __forceinline__ void blocks_heads(const RopeBlocksArgs& a, int which, int b, int j,
+                                             int h0, int h1, const int* s_tok) {
   constexpr int kSlots = D / 16, kVecs = D / 8;
   constexpr int kRowStep = kBlocksThreads / kSlots, kRows = kBlk / kRowStep;
   constexpr int kAhead = 2;
@@ -176,7 +178,7 @@ __device__ __forceinline__ void blocks_heads(const RopeBlocksArgs& a, int which,
   const long long bN = static_cast<long long>(b) * a.N;
   const long long dst_step = a.blk_stride * kBlk * kVecs;
   uint4* dst = a.dst[which] + (static_cast<long long>(b) * a.Hh + h0) * dst_step +
-               (static_cast<long long>(a.base_block + blockIdx.x) * kBlk + row0) * kVecs;
+               (static_cast<long long>(a.base_block + j) * kBlk + row0) * kVecs;
   int va, vb;
   slot_vectors<D, MODE>(a.rope.P, slot, va, vb);
   const uint4* src[kRows];  // the row of head h0; null for a pad row
@@ -253,24 +255,19 @@ rope_blocks_kernel(RopeBlocksArgs a) {
   pdl_wait();     // global memory only after the predecessor grid completed
   pdl_trigger();
   __shared__ int s_tok[kBlk];
-  const int j = blockIdx.x;
-  const int b = blockIdx.z / a.tensors;
-  const int which = blockIdx.z % a.tensors;
-  const int slot0 = j * kBlk;
+  const RunAt at(a.runs, a.nb, a.B, a.Hh);
+  const int slot0 = at.j * kBlk;
   const int valid = min(kBlk, a.N - slot0);
-  const bool first_cta = blockIdx.y == 0 && blockIdx.z == 0;
-  find_block_tokens<kBlocksThreads>(a.perm, a.N, slot0, valid, s_tok, j == 0 && first_cta,
+  find_block_tokens<kBlocksThreads>(a.perm, a.N, slot0, valid, s_tok, at.j == 0 && at.first,
                                     a.d_err, a.T, a.H, a.W);
-  if (first_cta && a.block_valid != nullptr && threadIdx.x == 0)
-    a.block_valid[a.base_block + j] = valid;
+  if (at.first && a.block_valid != nullptr && threadIdx.x == 0)
+    a.block_valid[a.base_block + at.j] = valid;
   // A slot of the chunk that no token maps to: perm is not a permutation.
-  if (first_cta && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
-  const int h0 = blockIdx.y * a.heads;
-  const int h1 = min(h0 + a.heads, a.Hh);
-  if (which == 0)
-    blocks_heads<D, MODE>(a, 0, b, h0, h1, s_tok);
+  if (at.first && threadIdx.x < valid && s_tok[threadIdx.x] < 0) report(a.d_err, BSA_DEV_BAD_PERM);
+  if (at.which == 0)
+    blocks_heads<D, MODE>(a, 0, at.b, at.j, at.h0, at.h1, s_tok);
   else
-    blocks_heads<D, kRopeNone>(a, 1, b, h0, h1, s_tok);
+    blocks_heads<D, kRopeNone>(a, 1, at.b, at.j, at.h0, at.h1, s_tok);
 }
 
 template <int D>
@@ -285,9 +282,10 @@ static bsa_status launch_tokens(int mode, const RopeTokensArgs& a, int B, cudaSt
 }
 
 template <int D>
-static bsa_status launch_blocks(int mode, const RopeBlocksArgs& a, int B, int nb, cudaStream_t s) {
-  dim3 grid(nb, (a.Hh + a.heads - 1) / a.heads, B * a.tensors);
-  const dim3 block(kBlocksThreads);
+static bsa_status launch_blocks(int mode, RopeBlocksArgs a, cudaStream_t s) {
+  const long long blocks = static_cast<long long>(a.nb) * a.B;
+  a.runs = head_runs(blocks, a.Hh, a.tensors);
+  const dim3 grid(run_ctas(a.runs, blocks, a.Hh, a.tensors)), block(kBlocksThreads);
   if (mode == kRopeInterleaved)
     return launch_pdl(rope_blocks_kernel<D, kRopeInterleaved>, grid, block, 0, s, a);
   if (mode == kRopeHalf) return launch_pdl(rope_blocks_kernel<D, kRopeHalf>, grid, block, 0, s, a);
@@ -394,13 +392,14 @@ extern "C" bsa_status bsa_tokens_to_blocks_rope(const void* x_tok, void* x_blk, 
   a.N = n;
   a.Hh = Hh;
   a.tensors = 1;
-  a.heads = heads_per_cta(static_cast<long long>(nb) * B, Hh, 1, 2.0);
+  a.nb = nb;
+  a.B = B;
   a.blk_stride = nb;
   a.T = T;
   a.H = H;
   a.W = W;
   cudaStream_t s = as_stream(stream);
-  BSA_TRY(D == 128 ? launch_blocks<128>(mode, a, B, nb, s) : launch_blocks<64>(mode, a, B, nb, s));
+  BSA_TRY(D == 128 ? launch_blocks<128>(mode, a, s) : launch_blocks<64>(mode, a, s));
   return x_mean == nullptr ? BSA_OK : launch_rows_mean(x_blk, x_mean, B, Hh, D, nb, n, s);
 }
 
@@ -433,15 +432,15 @@ extern "C" bsa_status bsa_kv_append_rope(bsa_kv_cache* c, const void* k_tok, con
   a.N = n;
   a.Hh = c->Hh;
   a.tensors = 2;
-  a.heads = heads_per_cta(2LL * nb * c->B, c->Hh, 1, 2.0);
+  a.nb = nb;
+  a.B = c->B;
   a.blk_stride = c->max_blocks;
   a.base_block = c->n_blocks;
   a.T = T;
   a.H = H;
   a.W = W;
   cudaStream_t s = as_stream(stream);
-  BSA_TRY(c->D == 128 ? launch_blocks<128>(mode, a, c->B, nb, s)
-                      : launch_blocks<64>(mode, a, c->B, nb, s));
+  BSA_TRY(c->D == 128 ? launch_blocks<128>(mode, a, s) : launch_blocks<64>(mode, a, s));
   if (c->kmean != nullptr) BSA_TRY(launch_block_means(c, c->n_blocks, nb, d_err, s));
   c->n_blocks += nb;
   return BSA_OK;

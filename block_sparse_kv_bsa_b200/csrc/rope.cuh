@@ -233,6 +233,63 @@ inline int heads_per_cta(long long others, int Hh, int per_sm, double start) {
   return best;
 }
 
+// The same for a chunk of `blocks` blocks whose K tiles (turned) and V tiles
+// (moved; `tensors` = 2) go to CTAs of their own, K's first, one CTA to an SM:
+// runs of heads for each, by the sum of the work over the SMs and the longest
+// run that may start last.  In head tiles, a K run's start (tokens, angles,
+// first loads) counts 2 and a V run's 1; the short V runs fill the SMs that K's
+// leave idle.
+struct HeadRuns {
+  int heads[2];
+};
+inline HeadRuns head_runs(long long blocks, int Hh, int tensors) {
+  HeadRuns best{{1, 1}};
+  double best_cost = -1.0;
+  for (int gk = 1; gk <= Hh && gk <= 32; ++gk) {
+    const int hk = (Hh + gk - 1) / gk;
+    const long long nk = blocks * ((Hh + hk - 1) / hk);
+    const double k_work = static_cast<double>(blocks) * Hh + 2.0 * nk;
+    const double k_time = static_cast<double>((nk + 147) / 148) * (hk + 2.0);
+    for (int gv = 1; gv <= (tensors == 2 ? Hh : 1) && gv <= 32; ++gv) {
+      const int hv = tensors == 2 ? (Hh + gv - 1) / gv : 0;
+      const long long nv = tensors == 2 ? blocks * ((Hh + hv - 1) / hv) : 0;
+      const double v_work = tensors == 2 ? static_cast<double>(blocks) * Hh + 1.0 * nv : 0.0;
+      const double all = (k_work + v_work) / 148.0 + (tensors == 2 ? 0.5 * (hv + 1.0) : 0.0);
+      const double cost = all > k_time ? all : k_time;
+      if (best_cost < 0.0 || cost < best_cost) {
+        best_cost = cost;
+        best.heads[0] = hk;
+        best.heads[1] = tensors == 2 ? hv : 1;
+      }
+    }
+  }
+  return best;
+}
+
+// What a CTA of such a grid works on.
+struct RunAt {
+  int which, b, j, h0, h1;
+  bool first;  // of its block
+  __device__ __forceinline__ RunAt(const HeadRuns& r, int nb, int B, int Hh) {
+    const int groups0 = (Hh + r.heads[0] - 1) / r.heads[0];
+    int x = blockIdx.x;
+    const int k_ctas = groups0 * nb * B;
+    which = x >= k_ctas;
+    if (which) x -= k_ctas;
+    j = x % nb;
+    x /= nb;
+    b = x % B;
+    h0 = x / B * r.heads[which];
+    h1 = min(h0 + r.heads[which], Hh);
+    first = !which && b == 0 && h0 == 0;
+  }
+};
+inline unsigned run_ctas(const HeadRuns& r, long long blocks, int Hh, int tensors) {
+  long long n = blocks * ((Hh + r.heads[0] - 1) / r.heads[0]);
+  if (tensors == 2) n += blocks * ((Hh + r.heads[1] - 1) / r.heads[1]);
+  return static_cast<unsigned>(n);
+}
+
 // Checks a descriptor and fills the kernel's arguments; `mode` is how the
 // kernels handle its layout.
 bsa_status rope_args(const bsa_rope_desc* d, int B, int D, int T, int H, int W, RopeArgs* out,
