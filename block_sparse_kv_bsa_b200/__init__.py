@@ -205,6 +205,10 @@ def _stream(device) -> ctypes.c_void_p:
 
 
 def _need(t: torch.Tensor, name: str, dtype, device=None, shape=None):
+    # The common case in few steps; what is wrong is found out below.
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (device is None or t.device == device) and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:

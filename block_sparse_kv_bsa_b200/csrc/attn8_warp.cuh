@@ -197,8 +197,6 @@ __device__ __forceinline__ float load_query_row(const __nv_bfloat16* r, uint32_t
   return qs;
 }
 
-// A tile's metadata: (key scale, log2 v, 1 / v, valid rows as int).
-
 // Moves a row's reference when a weight would pass 2^kPMaxLog2; returns what O
 // (and l, done here) must be multiplied by.
 __device__ __forceinline__ float move_reference(float mx, float& m, float& l) {
