@@ -71,10 +71,9 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) 
 
 // Power-of-two scale of a query row whose largest magnitude is amax: q / scale
 // then has its largest magnitude in [2^13, 2^14), and everything down to
-// 2^-28 of it is exact in f16.  A row that is zero, or holds an infinity or
-// NaN, is not scaled.
+// 2^-28 of it is exact in f16.  A zero row is not scaled.
 __device__ __forceinline__ float q_row_scale(float amax) {
-  if (!(amax > 0.f && amax <= 3.402823466e38f)) return 1.f;
+  if (!(amax > 0.f)) return 1.f;
   int e = (__float_as_int(amax) >> 23) - 127 - 13;  // subnormal amax: e = -140
   e = e < -126 ? -126 : e;
   return pow2i(e);
@@ -154,7 +153,8 @@ struct KeyTile {
 
 // A lane's part of a query row r (null: zeros) as f16 pairs over the row's
 // power-of-two scale, which is returned: lo[ks], hi[ks] are elements {0, 1} and
-// {2, 3} of k step ks.
+// {2, 3} of k step ks.  A row with an infinity or a NaN has no softmax: its scale,
+// and through it all it leads to, is NaN.
 template <int D>
 __device__ __forceinline__ float load_query_row(const __nv_bfloat16* r, uint32_t (&lo)[D / 16],
                                                 uint32_t (&hi)[D / 16]) {
@@ -182,7 +182,7 @@ __device__ __forceinline__ float load_query_row(const __nv_bfloat16* r, uint32_t
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     bad |= __shfl_xor_sync(0xffffffffu, static_cast<int>(bad), off) != 0;
   }
-  const float qs = bad ? 1.f : q_row_scale(amax);
+  const float qs = bad ? __int_as_float(0x7fffffff) : q_row_scale(amax);
   const float inv = 1.f / qs;  // exact: a power of two
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {

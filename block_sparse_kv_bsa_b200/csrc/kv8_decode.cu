@@ -15,8 +15,6 @@
 
 namespace bsa {
 
-
-
 constexpr int kDecWarps = 8;                          // consumers: 16 keys of each block
 constexpr int kDecThreads = kDecWarps * 32 + 32;      // and one producer warp
 constexpr int kDecSlots = 148;     // CTAs resident at once: one on each SM
@@ -61,6 +59,12 @@ __device__ __forceinline__ long long query_row(const Decode8Args& a, long long b
   const long long b = bh / a.Hh;
   const int h = static_cast<int>(bh % a.Hh);
   return (b * a.n_tok + r / a.group) * a.Hq + h * a.group + r % a.group;
+}
+
+// Whether a row saw a key: its sum is zero and its reference unset only without
+// one (logits that are all NaN leave the reference unset and the sum NaN).
+__device__ __forceinline__ bool row_has_keys(float m, float l) {
+  return m > -INFINITY || l != 0.f;
 }
 
 // W is AttnWarp16<D>, or AttnWarp8<D> for at most 8 rows in all.
@@ -221,7 +225,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
       o = fmaf(s_o[(k * 16 + r) * kStride + c], f, o);
     }
     if (a.n_split == 1) {
-      const bool have = m > -INFINITY;
+      const bool have = row_has_keys(m, l);
       const long long out = query_row(a, bh, tile * 16 + r);
       a.o[out * D + out_element<D>(c)] = __float2bfloat16(have ? o / l : 0.f);
       if (c == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
@@ -288,7 +292,7 @@ decode8_join_kernel(Decode8Args a) {
   float o = 0.f;
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) o += s_acc[w][threadIdx.x];
-  const bool have = m > -INFINITY;
+  const bool have = row_has_keys(m, l);
   const long long out = query_row(a, bh, row);
   a.o[out * D + out_element<D>(threadIdx.x)] = __float2bfloat16(have ? o / l : 0.f);
   if (threadIdx.x == 0) a.lse[out] = have ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;

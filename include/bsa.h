@@ -589,7 +589,10 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
  *   idx,cnt  device int32 [B, Hh, n_q_blocks, max_sel], [B, Hh, n_q_blocks]
  *   o_blk    device bf16, q_blk's shape;  lse device fp32 [B, Hq, n_q_blocks*128]
  * Everything else is bsa_attn's.  Rows of a block past its valid count are
- * never read as values: what they hold (NaN included) does not matter.
+ * never read as values: what they hold (NaN included) does not matter.  A query
+ * row with an infinity or a NaN gets NaN for its O and LSE.  Weights are held
+ * times their block's value scale: value scales of one route have to lie within
+ * a factor of 2^100 of each other.
  * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh;
  *         on the device also BSA_DEV_BAD_SCALE.
  */
@@ -613,7 +616,8 @@ bsa_status bsa_kv8_attn_decode_workspace_size(int B, int Hq, int Hh, int D, int 
  *   idx,cnt  device int32 [B, Hh, max_sel], [B, Hh], or both NULL: every
  *            block in use, [0, n_blocks) (max_sel is then not read)
  *   o_tok    device bf16 [B, n_tok, Hq, D];  lse device fp32 [B, n_tok, Hq]
- * A query with an empty route gets O = 0 and LSE = -inf.
+ * A query with an empty route gets O = 0 and LSE = -inf, one with an infinity
+ * or a NaN gets NaN.  Value scales as for bsa_kv8_attn.
  *   workspace  device, at least bsa_kv8_attn_decode_workspace_size bytes,
  *              256-aligned; calls that may overlap need one each
  * Errors: those of bsa_kv8_attn; BSA_ERR_CAPACITY (workspace too small);

@@ -446,6 +446,32 @@ def test_decode8_equals_the_block_form():
         ref.check_attn(o[0, h, :5], lse[0, h, :5], *want)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n_tok,blocks", [(3, 1), (3, 40), (9, 40)])
+def test_decode8_special_queries_stay_in_their_rows(D, n_tok, blocks):
+    # A softmax over logits that are NaN or infinite has no value: NaN, as in the
+    # block form, and nothing of it in the rows beside it.
+    cache = ref.fill_cache(bsa, 1, 1, D, blocks, [128] * (blocks - 1) + [50], 95)
+    q = tokens(1, n_tok, 2, D, 96)
+    o, lse = bsa.bsa_kv8_attn_decode(q, cache)
+    q2 = q.clone()
+    q2[0, 0, 1, 3] = float("nan")
+    q2[0, 1, 0, 7] = float("-inf")
+    q2[0, 2] = float("inf")
+    o2, lse2 = bsa.bsa_kv8_attn_decode(q2, cache)
+    odd = torch.zeros((n_tok, 2), dtype=torch.bool, device=DEV)
+    odd[0, 1] = odd[1, 0] = odd[2, 0] = odd[2, 1] = True
+    assert torch.equal(o[0][~odd], o2[0][~odd]) and torch.equal(lse[0][~odd], lse2[0][~odd])
+    assert torch.isnan(o2[0][odd]).all() and torch.isnan(lse2[0][odd]).all()
+    q_blk = torch.zeros((1, 2, 128, D), dtype=torch.bfloat16, device=DEV)
+    q_blk[:, :, :n_tok] = q2.transpose(1, 2)
+    idx = torch.arange(blocks, dtype=torch.int32, device=DEV).view(1, 1, 1, blocks)
+    cnt = torch.full((1, 1, 1), blocks, dtype=torch.int32, device=DEV)
+    ob, lb = bsa.bsa_kv8_attn(q_blk, cache, idx, cnt)
+    odd = odd.T
+    assert torch.isnan(ob[0, :, :n_tok][odd]).all() and torch.isnan(lb[0, :, :n_tok][odd]).all()
+
+
 # ---------------------------------------------------------------------------
 # Together
 # ---------------------------------------------------------------------------
