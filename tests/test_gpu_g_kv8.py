@@ -476,6 +476,50 @@ def test_decode8_special_queries_stay_in_their_rows(D, n_tok, blocks):
 # Together
 # ---------------------------------------------------------------------------
 
+def test_route_calls_take_the_8bit_cache():
+    # They read the pooled keys alone: the same routes as from a bf16 cache with
+    # the same pooled keys.  The calls that would read bf16 keys refuse it.
+    B, Hh, D, hist, own = 2, 3, 128, 70, 2
+    valid = [128] * (hist + own - 1) + [77]
+    c8 = ref.fill_cache(bsa, B, Hh, D, hist + own, valid, 101)
+    g = torch.Generator(device=DEV).manual_seed(102)
+    kmean = torch.randn((B, Hh, hist + own, D), generator=g, device=DEV)
+    c8 = bsa.KVCache8.from_tensors(c8.k, c8.k_scale, c8.v, c8.v_scale, c8.block_valid, hist + own,
+                                   kmean)
+    c16 = bsa.KVCache(B, Hh, D, hist + own, device=DEV, pooled_keys=True)
+    c16.block_valid.copy_(c8.block_valid)
+    c16.kmean.copy_(kmean)
+    c16.n_blocks = hist + own
+    q = torch.randn((B, Hh, own * 128, D), generator=g, device=DEV).to(torch.bfloat16)
+    qm = torch.randn((B, Hh, own, D), generator=g, device=DEV)
+    prior = torch.rand((B, own, hist), generator=g, device=DEV)
+    for call in (lambda c: bsa.bsa_route(q, c, hist, hist, own, 9, g=prior),
+                 lambda c: bsa.bsa_route_qmean(qm, c, hist, hist, own, 9, g=prior),
+                 lambda c: bsa.bsa_route_velox(q, c, hist, hist, own, g=prior, k_cov=9, k_unc=20),
+                 lambda c: bsa.bsa_route_velox(None, c, hist, hist, own, g=prior, k_cov=9,
+                                               k_unc=20, q_mean=qm)):
+        (i8, n8), (i16, n16) = call(c8), call(c16)
+        bsa.raise_on_device_error(DEV)
+        assert torch.equal(n8, n16)
+        live = torch.arange(i8.shape[-1], device=DEV) < n8[..., None]
+        assert torch.equal(i8[live], i16[live])
+    idx, cnt = bsa.bsa_route_qmean(qm, c8, hist, hist, own, 9)
+    k = tokens(B, 256, Hh, D, 103)
+    bare = bsa.KVCache8.from_tensors(c8.k, c8.k_scale, c8.v, c8.v_scale, c8.block_valid,
+                                     hist + own)
+    for call in (lambda: bsa.bsa_attn(q, c8, idx, cnt),
+                 lambda: bsa.bsa_kv_append(c8, k, k, 1, 16, 16),
+                 lambda: bsa.bsa_kv_pool_means(c8),
+                 lambda: bsa.bsa_route_qmean(qm, bare, hist, hist, own, 9)):
+        with pytest.raises((bsa.BsaError, ValueError, TypeError)):
+            call()
+    for call in (lambda: bsa.bsa_kv8_attn(q, c16, idx, cnt),
+                 lambda: bsa.bsa_kv8_attn_decode(q[:, :, :1].transpose(1, 2).contiguous(), c16),
+                 lambda: bsa.bsa_kv8_append(c16, k, k, 1, 16, 16)):
+        with pytest.raises(TypeError):
+            call()
+
+
 def run_step(state):
     """One rollout step on the 8-bit cache: append, Q to blocks with means, route
     from the pooled keys, attention, O to tokens, then a few decode tokens."""
