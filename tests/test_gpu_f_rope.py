@@ -210,3 +210,24 @@ def test_wrappers_refuse():
     with pytest.raises(bsa.BsaError):
         bsa.bsa_kv_append_rope(cache, x, x, 6, 1, 1, rope)
     assert cache.n_blocks == 1
+
+
+def test_offsets_past_32_bits():
+    # Tensors of more than 2^31 elements: the last tokens, batch entries and blocks
+    # give the bits of a call on those alone.
+    g = torch.Generator(device=DEV).manual_seed(61)
+    _, rope = make((64,), "half")
+    N, Hh, D, last = (1 << 20) + 5, 17, 128, 6
+    x = torch.randn((1, N, Hh, D), generator=g, device=DEV, dtype=torch.bfloat16)
+    part = x[:, -last:].contiguous()
+    want = bsa.bsa_rope(part, last, 1, 1, rope, origin=(N - last, 0, 0))
+    bsa.bsa_rope(x, N, 1, 1, rope, out=x)
+    assert torch.equal(x[:, -last:], want)
+    del x
+    _, rope = make((22, 21, 21), "interleaved")
+    B, T, H, W, Hh = 9, 8, 32, 64, 120
+    x = torch.randn((B, T * H * W, Hh, D), generator=g, device=DEV, dtype=torch.bfloat16)
+    blk = bsa.bsa_tokens_to_blocks_rope(x, T, H, W, rope)
+    part = bsa.bsa_tokens_to_blocks_rope(x[B - 1:], T, H, W, rope)
+    assert torch.equal(blk[B - 1:], part)
+    bsa.raise_on_device_error(DEV)

@@ -520,6 +520,35 @@ def test_route_calls_take_the_8bit_cache():
             call()
 
 
+def test_offsets_past_32_bits():
+    # The last blocks of a cache of more than 2^32 bytes a tensor give the bits of
+    # a small cache with the same blocks.
+    Hh, D, T, H, W, big = 2, 128, 1, 16, 20, 135000
+    N, nb = T * H * W, 3
+    k, v = tokens(1, N, Hh, D, 111), tokens(1, N, Hh, D, 112)
+    q, qd = tokens(1, 128, Hh, D, 113), tokens(1, 12, Hh, D, 114)
+    q = q.transpose(1, 2).contiguous()
+    _, rope = make((22, 21, 21), "half")
+    got = []
+    for blocks in (nb, big):
+        cache = bsa.KVCache8(1, Hh, D, blocks, device=DEV, pooled_keys=True)
+        first = cache.n_blocks = blocks - nb
+        assert bsa.bsa_kv8_append(cache, k, v, T, H, W, rope=rope) == first
+        idx = torch.arange(first, blocks, dtype=torch.int32, device=DEV).expand(1, Hh, 1, nb)
+        idx = idx.contiguous()
+        cnt = torch.full((1, Hh, 1), nb, dtype=torch.int32, device=DEV)
+        out = bsa.bsa_kv8_attn(q, cache, idx, cnt)
+        out += bsa.bsa_kv8_attn_decode(qd, cache, idx[:, :, 0].contiguous(),
+                                       cnt[:, :, 0].contiguous())
+        bsa.raise_on_device_error(DEV)
+        got.append(out + tuple(t[:, :, first:].view(torch.uint8).clone() for t in
+                               (cache.k, cache.v, cache.k_scale, cache.v_scale, cache.kmean)))
+        del cache
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+    assert torch.isfinite(got[0][0].float()).all()
+
+
 def run_step(state):
     """One rollout step on the 8-bit cache: append, Q to blocks with means, route
     from the pooled keys, attention, O to tokens, then a few decode tokens."""
