@@ -200,7 +200,9 @@ __device__ __forceinline__ float load_query_row(const __nv_bfloat16* r, uint32_t
 // Moves a row's reference when a weight would pass 2^kPMaxLog2; returns what O
 // (and l, done here) must be multiplied by.
 __device__ __forceinline__ float move_reference(float mx, float& m, float& l) {
-  if (!(mx > m + kPMaxLog2)) return 1.f;
+  // The difference of near values is exact; m + 15 rounds to m + 16 from 2^24 on,
+  // and a weight of 2^16 is no f16.
+  if (!(mx - m > kPMaxLog2)) return 1.f;
   const float next = mx - kPBias;
   const float fix = ex2_approx(m - next);
   m = next;

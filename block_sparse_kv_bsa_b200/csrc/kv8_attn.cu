@@ -611,7 +611,9 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         bar_sync8(bar_in, 64);
         m_prev = lds_f(tok_other);
       }
-      const float m_t = (t == 0 || mx > m_prev + kMoveAt) ? mx - kBias : m_prev;
+      // (the difference, which is exact for near values: m_prev + 15 rounds to
+      // m_prev + 16 from 2^24 on, and a weight of 2^16 is no f16)
+      const float m_t = (t == 0 || mx - m_prev > kMoveAt) ? mx - kBias : m_prev;
       if (t + 1 < n) {
         sts_f(tok_mine, m_t);
         bar_arrive8(bar_out, 64);
