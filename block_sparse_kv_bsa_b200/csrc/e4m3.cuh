@@ -41,14 +41,25 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// A block scale as read: one that is not finite and positive is reported and
-// counts as 1.
-__device__ __forceinline__ float checked_scale(float s, int32_t* d_err) {
-  if (!(s > 0.f && s <= 3.402823466e38f)) {
+// Smallest value scale, 2^-80.  A row's sum is held as the sum of weight / v with
+// weights of up to 2^15, so 2^31 keys stay below 2^126.  The append writes no
+// scale below 2^-64 / 448.
+constexpr float kVScaleMin = 8.271806125530277e-25f;
+
+// A block scale as read: one that is not finite and positive, or a value scale
+// below its bound, is reported and counts as 1.
+__device__ __forceinline__ float checked_scale(float s, float least, int32_t* d_err) {
+  if (!(s > 0.f && s >= least && s <= 3.402823466e38f)) {
     report(d_err, BSA_DEV_BAD_SCALE);
     return 1.f;
   }
   return s;
+}
+__device__ __forceinline__ float checked_k_scale(float s, int32_t* d_err) {
+  return checked_scale(s, 0.f, d_err);
+}
+__device__ __forceinline__ float checked_v_scale(float s, int32_t* d_err) {
+  return checked_scale(s, kVScaleMin, d_err);
 }
 
 }  // namespace bsa

@@ -397,8 +397,8 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
         if (t < n) {
           const int blk = clamp_block(a, route[t]);
           valid = a.block_valid[blk];
-          ks = checked_scale(a.k_scale[bh * a.max_blocks + blk], a.d_err);
-          vs = checked_scale(a.v_scale[bh * a.max_blocks + blk], a.d_err);
+          ks = checked_k_scale(a.k_scale[bh * a.max_blocks + blk], a.d_err);
+          vs = checked_v_scale(a.v_scale[bh * a.max_blocks + blk], a.d_err);
           if (valid < 1 || valid > kBlk) {
             report(a.d_err, BSA_DEV_BAD_VALID);
             valid = valid < 1 ? 1 : kBlk;

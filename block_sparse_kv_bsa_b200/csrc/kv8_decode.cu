@@ -151,8 +151,8 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         report(a.d_err, BSA_DEV_BAD_VALID);
         valid = valid < 1 ? 1 : kBlk;
       }
-      ks = checked_scale(ks, a.d_err);
-      vs = checked_scale(vs, a.d_err);
+      ks = checked_k_scale(ks, a.d_err);
+      vs = checked_v_scale(vs, a.d_err);
       const uint4 meta = make_uint4(__float_as_uint(ks), __float_as_uint(log2f(vs)),
                                     __float_as_uint(1.f / vs), static_cast<uint32_t>(valid));
       for (int i = 0; ok && i < 32 && c0 + i < count; ++i) {

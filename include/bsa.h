@@ -72,7 +72,8 @@ typedef enum bsa_status {
 #define BSA_DEV_BAD_VALID 3    /* a block_valid entry outside [1, 128] */
 #define BSA_DEV_BAD_PERM 4     /* a permutation entry outside the chunk */
 #define BSA_DEV_WAIT_TIMEOUT 5 /* a bounded pipeline wait gave up */
-#define BSA_DEV_BAD_SCALE 6    /* an 8-bit block scale that is not finite and > 0 */
+#define BSA_DEV_BAD_SCALE 6    /* an 8-bit block scale that is not finite and > 0, or
+                                  a value scale below 2^-80 */
 
 /*
  * Caller-owned view of the block KV cache.
@@ -542,9 +543,10 @@ bsa_status bsa_kv_append_rope(bsa_kv_cache *cache, const void *k_tok, const void
  * A block KV cache held in 8 bits: e4m3 codes with one fp32 scale per block
  * of 128 tokens and head.  A key is code * k_scale, a value code * v_scale.
  *   k, v              device e4m3 [B, Hh, max_blocks, 128, D], 16-byte aligned
- *   k_scale, v_scale  device fp32 [B, Hh, max_blocks]: finite and > 0 for
- *                     every block in use (else BSA_DEV_BAD_SCALE, and the
- *                     block's scale counts as 1)
+ *   k_scale, v_scale  device fp32 [B, Hh, max_blocks]: finite and > 0, and
+ *                     v_scale at least 2^-80, for every block in use (else
+ *                     BSA_DEV_BAD_SCALE, and the block's scale counts as 1).
+ *                     bsa_kv8_append writes none below 2^-64 / 448.
  * The rest is bsa_kv_cache's.  kmean, when present, makes the router work on
  * this cache: the route calls take a bsa_kv_cache with k = v = NULL and this
  * cache's block_valid, kmean and sizes.
@@ -590,9 +592,12 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
  *   o_blk    device bf16, q_blk's shape;  lse device fp32 [B, Hq, n_q_blocks*128]
  * Everything else is bsa_attn's.  Rows of a block past its valid count are
  * never read as values: what they hold (NaN included) does not matter.  A query
- * row with an infinity or a NaN gets NaN for its O and LSE.  Weights are held
- * times their block's value scale: value scales of one route have to lie within
- * a factor of 2^100 of each other.
+ * row with an infinity or a NaN gets NaN for its O and LSE.  Logits have to stay
+ * within fp32's range, and value scales of one route within a factor of 2^100
+ * of each other.  Weights are held in f16 times their block's value scale: such a
+ * product is rounded by 2^-11 of itself, but by 2^-32 of the row's largest where
+ * it is 2^21 or more below that, so beside a block of far larger value scale the
+ * values of another keep only that absolute accuracy.
  * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh;
  *         on the device also BSA_DEV_BAD_SCALE.
  */

@@ -82,3 +82,89 @@ def test_huge_and_tiny_query_rows_stay_finite():
                 _, vals = ref.gather(cache, 0, h, range(13))
                 top = np.abs(vals).max(0) * (1 + ref.BF16 + ref.WEIGHT) + 1e-30
                 assert (np.abs(ref.f64(o[0, h])) <= top).all()
+
+
+# ---------------------------------------------------------------------------
+# Value scales
+# ---------------------------------------------------------------------------
+
+V_SCALE_MIN = 2.0 ** -80
+
+
+def flat_cache(blocks, D=64):
+    """Zero keys (every weight is the same), values of one to three, scales of one."""
+    cache = bsa.KVCache8(1, 1, D, blocks, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    cache.v.copy_(codes(torch.randint(1, 4, cache.v.shape, generator=g, device=DEV).float()))
+    cache.block_valid.fill_(128)
+    cache.n_blocks = blocks
+    return cache
+
+
+def test_smallest_value_scale_over_a_long_route():
+    # The row sum, weights over the value scale, at the scale's bound: 301
+    # thousand keys of the same weight.
+    cache = flat_cache(2352)
+    cache.v_scale.fill_(V_SCALE_MIN)
+    vals = ref.f64(cache.v[0, 0].float()).reshape(-1, 64) * V_SCALE_MIN
+    q = torch.ones((1, 1, 128, 64), dtype=torch.bfloat16, device=DEV)
+    for o, lse in both_forms(q, cache, (1, 12)):
+        assert (np.abs(ref.f64(lse) - np.log(2352 * 128)) <= 2.0 ** -16 + 2.0 ** -20 * 13).all()
+        want = vals.mean(0)
+        # The weights are equal powers of two: only the result is rounded, and the
+        # fp32 sums of 301 thousand terms.
+        assert (np.abs(ref.f64(o) - want) <= (ref.BF16 + 2.0 ** -9) * want).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -81, 2.0 ** -105, 1e-45, 0.0, -1.0, float("inf")])
+def test_value_scales_outside_their_bounds_are_reported(scale):
+    # They count as 1, whatever they are.
+    cache = flat_cache(40)
+    q = torch.ones((1, 1, 128, 64), dtype=torch.bfloat16, device=DEV)
+    want = both_forms(q, cache, (1,))
+    cache.v_scale[0, 0, 7] = scale
+    idx = torch.arange(40, dtype=torch.int32, device=DEV).view(1, 1, 1, 40)
+    cnt = torch.full((1, 1, 1), 40, dtype=torch.int32, device=DEV)
+    got = bsa.bsa_kv8_attn(q, cache, idx, cnt)
+    assert bsa.bsa_check_device_error(DEV) == (6, 6)
+    assert torch.equal(got[0], want[0][0]) and torch.equal(got[1], want[0][1])
+    got = bsa.bsa_kv8_attn_decode(q[:, :, :1].transpose(1, 2).contiguous(), cache)
+    assert bsa.bsa_check_device_error(DEV) == (6, 6)
+    assert torch.equal(got[0], want[1][0].transpose(1, 2))
+    # A key scale has no such bound, as long as it is positive and finite.
+    cache.v_scale.fill_(1.0)
+    cache.k_scale.fill_(scale if 0.0 < scale < float("inf") else 2.0 ** -126)
+    for x, y in zip(both_forms(q, cache, (1,)), want):
+        assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
+@pytest.mark.parametrize("spread", [0, 10, 20, 21, 30, 40, 64, 100])
+@pytest.mark.parametrize("big_first", [False, True])
+def test_value_scales_far_apart(spread, big_first):
+    # Blocks whose values are 2^spread times those of the others, with weights
+    # alike; in half of the columns the large blocks' values are zero, so the small
+    # ones' are seen there.
+    blocks, low = 6, V_SCALE_MIN if spread == 100 else 2.0 ** -9
+    cache = ref.fill_cache(bsa, 1, 1, 64, blocks, [128, 128, 50, 128, 128, 9], 31, k_gain=0.5)
+    big = torch.arange(blocks, device=DEV) % 2 == (0 if big_first else 1)
+    cache.v_scale.copy_(torch.where(big, low * 2.0 ** spread, low).view(1, 1, blocks))
+    cache.v.view(torch.uint8)[:, :, big, :, 32:] = 0
+    g = torch.Generator(device=DEV).manual_seed(32)
+    q = torch.randn((1, 1, 128, 64), generator=g, device=DEV).to(torch.bfloat16)
+    keys, vals = ref.gather(cache, 0, 0, range(blocks))
+    s = ref.f64(q[0, 0]) @ keys.T * ref.sm(64)
+    w = np.exp(s - s.max(-1, keepdims=True))
+    w /= w.sum(-1, keepdims=True)
+    v = np.concatenate([np.full(n, float(cache.v_scale[0, 0, j]))
+                        for j, n in enumerate(cache.block_valid.tolist())])
+    top = (w * v).max(-1, keepdims=True)                 # largest weight * scale of a row
+    want, lse_want, ra = ref.attend(ref.f64(q[0, 0]), keys, vals, ref.sm(64))
+    # A weight * scale is off by WEIGHT of itself or by 2^-32 of the row's largest,
+    # which every code is multiplied with.
+    flush = 2.0 ** -32 * top * np.abs(vals / v[:, None]).sum(0)
+    for o, lse in both_forms(q, cache, (1, 12)):
+        n = o.shape[2]
+        tol = (ref.BF16 * np.abs(want) + ref.WEIGHT * (1 + ref.BF16) * ra + flush)[:n]
+        assert (np.abs(ref.f64(o[0, 0]) - want[:n]) <= tol).all()
+        ltol = 2.0 ** -16 + 2.0 ** -20 * (np.abs(lse_want) + spread)
+        assert (np.abs(ref.f64(lse[0, 0]) - lse_want[:n]) <= ltol[:n]).all()
