@@ -508,8 +508,11 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       const int valid = lds_i(smem_u32(sm + L::kMeta) + (t % (2 * kMetaTiles)) * 16 + 12);
       if (t % kMetaTiles == kMetaTiles - 1) mbar_arrive(&bars[A_META_EMPTY + meta_half(t)]);
       const int s8 = t % kV8Slots, sl = t % kV16Slots;
-      // The whole warp passes each wait together: lanes that saw it complete at
-      // different polls measured stale codes in their first load now and then.
+      // Three orders keep the staging slot whole.  Every lane waits itself: its
+      // acquire makes the copied bytes visible to it.  The loads are volatile, so
+      // they stay between the wait and the arrival.  And a proxy fence stands
+      // before the arrival: the refill writes the slot through the async proxy,
+      // and the arrival alone orders these reads before generic accesses only.
       ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_V8_FULL + s8], (t / kV8Slots) & 1,
                                                      s_abort, kWait8));
       if (!ok) break;
@@ -517,6 +520,7 @@ attn8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ C
       uint2 x[kPer];
 #pragma unroll
       for (int u = 0; u < kPer; ++u) x[u] = lds_v2(src + u * (kConvert8 * 8));
+      fence_proxy_async_smem();
       mbar_arrive(&bars[A_V8_EMPTY + s8]);
       if (t >= kV16Slots) {
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&bars[A_V_EMPTY + sl],

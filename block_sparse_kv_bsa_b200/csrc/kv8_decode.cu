@@ -194,6 +194,7 @@ decode8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__
         W::Tile::load_keys(kt, kt + L::kTile, warp * 16, valid, x);
         w.step(x, warp * 16, meta);
       }
+      fence_proxy_async_smem();  // these reads before the refill, an async-proxy write
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[st]);
     }

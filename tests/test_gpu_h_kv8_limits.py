@@ -168,3 +168,33 @@ def test_value_scales_far_apart(spread, big_first):
         assert (np.abs(ref.f64(o[0, 0]) - want[:n]) <= tol).all()
         ltol = 2.0 ** -16 + 2.0 ** -20 * (np.abs(lse_want) + spread)
         assert (np.abs(ref.f64(lse[0, 0]) - lse_want[:n]) <= ltol[:n]).all()
+
+
+# ---------------------------------------------------------------------------
+# Repeats
+# ---------------------------------------------------------------------------
+
+def test_attn8_repeats_its_bits_over_many_tiles():
+    # 12 million tiles of long routes over a cache larger than L2: a tile read
+    # before it is whole, or overwritten while it is read, shows as a changed bit
+    # even where that happens once in two million tiles (six expected).
+    Hh, D, nqb, blocks, n = 24, 128, 49, 2352, 113
+    cache = ref.fill_cache(bsa, 1, Hh, D, blocks, [128] * (blocks - 1) + [96], 55)
+    g = torch.Generator(device=DEV).manual_seed(56)
+    q = (torch.randn((1, Hh, nqb * 128, D), generator=g, device=DEV) * 3).to(torch.bfloat16)
+    idx = torch.rand((1, Hh, nqb, blocks), generator=g, device=DEV).topk(n).indices
+    idx = idx.to(torch.int32).contiguous()
+    cnt = torch.full((1, Hh, nqb), n, dtype=torch.int32, device=DEV)
+    want = bsa.bsa_kv8_attn(q, cache, idx, cnt)
+    got = [torch.empty_like(t) for t in want]
+    for _ in range(91):
+        bsa.bsa_kv8_attn(q, cache, idx, cnt, o=got[0], lse=got[1])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # The ring of the few-token form: 56 thousand tiles a call.
+    for n_tok in (1, 12):
+        qt = q[:, :, :n_tok].transpose(1, 2).contiguous()
+        want = bsa.bsa_kv8_attn_decode(qt, cache)
+        for _ in range(50):
+            got = bsa.bsa_kv8_attn_decode(qt, cache)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    bsa.raise_on_device_error(DEV)
