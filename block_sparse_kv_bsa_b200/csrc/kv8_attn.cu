@@ -8,11 +8,14 @@
 //   S = Q K^T  runs on 8-bit operands (kind::f8f6f4), K tiles straight from the
 //     cache.  A bf16 has 8 significant bits, an e4m3 code 4 and an e5m2 code 3:
 //     with q scaled by a power of two per row, q = q1 + q2 with q1 = e4m3(q) and
-//     q2 = e5m2(q - q1) is exact (the rest of an 8-bit significand after its
-//     nearest 4-bit one is at most 8 units, and 0 to 8 all have 3 bits) for
-//     elements down to 2^-14 of the row's largest; below, the error is at most
-//     2^-21 of the largest.  Two 8-bit products cost what one bf16 product
-//     costs, and K needs no conversion.
+//     q2 = e5m2(q - q1) is exact while q1 is a normal e4m3 (the rest of an 8-bit
+//     significand after its nearest 4-bit one is at most 8 units, and 0 to 8 all
+//     have 3 bits).  The row's largest is scaled to [2^7, 2^8) and e4m3 is normal
+//     from 2^-6 on, so that holds for elements down to 2^-13 of the largest;
+//     below, q1 has the step 2^-9 and the error is at most 2^-14, 2^-21 of the
+//     largest (for rows whose largest is 2^-119 or more: the scale is no
+//     subnormal).  Two 8-bit products cost what one bf16 product costs, and K
+//     needs no conversion.
 //   O += P V  runs on f16 operands: P needs more range than e4m3 has (many
 //     small weights beside a large one would be rounded away), so a warpgroup
 //     converts each V tile from e4m3 to f16 (exact) in shared memory.

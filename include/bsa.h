@@ -584,7 +584,7 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
  * bsa_attn over an 8-bit cache, with grouped heads: Hq query heads, a
  * multiple of the cache's Hh; query head h reads cache head h / (Hq / Hh) and
  * that head's route.  Products run on the tensor core with fp32 accumulation;
- * codes and bf16 queries enter them exactly (query elements below 2^-14 of
+ * codes and bf16 queries enter them exactly (query elements below 2^-13 of
  * their row's largest with an error of at most 2^-21 of it), and the softmax
  * weights are rounded to f16.
  *   q_blk    device bf16 [B, Hq, n_q_blocks*128, D]

@@ -198,3 +198,35 @@ def test_attn8_repeats_its_bits_over_many_tiles():
             got = bsa.bsa_kv8_attn_decode(qt, cache)
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     bsa.raise_on_device_error(DEV)
+
+
+# ---------------------------------------------------------------------------
+# Query elements far below their row's largest
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_query_elements_are_exact_down_to_2_to_the_minus_13(D):
+    # Row r holds 1 and 2^-e (1 + r / 128); one key of code 448 sees the latter
+    # alone, so the LSE is that element as the products saw it, times 448.
+    cache = bsa.KVCache8(1, 1, D, 1, device=DEV)
+    k = torch.zeros((1, 1, 1, 128, D), device=DEV)
+    k[..., 0, 1] = 448.0
+    cache.k.copy_(codes(k))
+    cache.block_valid.fill_(1)
+    cache.n_blocks = 1
+    mant = 1 + torch.arange(128, device=DEV).float() / 128
+    for e in range(1, 18):
+        q = torch.zeros((1, 1, 128, D), device=DEV)
+        q[..., 0] = 1.0
+        q[0, 0, :, 1] = mant * 2.0 ** -e
+        forms = both_forms(q.to(torch.bfloat16), cache, (8, 128), sm_scale=2.0 ** e)
+        want = 448.0 * ref.f64(mant)
+        for i, (_, lse) in enumerate(forms):
+            n = lse.shape[2]
+            err = np.abs(ref.f64(lse[0, 0]) - want[:n])
+            tol = 2.0 ** -16 + 2.0 ** -20 * want[:n]
+            # Past 2^-13 the block form may be off by 2^-21 of the row's largest; the
+            # few-token form holds 2^-28.
+            assert (err <= tol + (448.0 * 2.0 ** (e - 21) if e > 13 and i == 0 else 0.0)).all(), e
+            if e == 14 and i == 0:
+                assert (err > tol).any()   # so 2^-13 is the bound, not a loose one
