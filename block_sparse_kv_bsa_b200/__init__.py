@@ -679,6 +679,20 @@ ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "by_parts": 3}
 
 
+def _whole(x) -> int:
+    """A position or a count as an int; a fraction is refused, not cut off."""
+    i = int(x)
+    if i != x:
+        raise TypeError(f"{x!r} is not a whole number")
+    return i
+
+
+def _chunk(T, H, W) -> Tuple[int, int, int]:
+    if type(T) is type(H) is type(W) is int:
+        return T, H, W
+    return _whole(T), _whole(H), _whole(W)
+
+
 def bsa_rope_frequencies(n_pairs: int, base: float = 10000.0, scaling: str = "none",
                          factor: float = 1.0, original_length: float = 1.0,
                          beta_fast: float = 32.0, beta_slow: float = 1.0
@@ -687,13 +701,14 @@ def bsa_rope_frequencies(n_pairs: int, base: float = 10000.0, scaling: str = "no
     of one axis; ``scaling`` is "none", "linear", "base" or "by_parts"."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    out = np.empty(max(int(n_pairs), 1), dtype=np.float64)
+    n_pairs = _whole(n_pairs)
+    out = np.empty(max(n_pairs, 1), dtype=np.float64)
     amp = ctypes.c_double(1.0)
     _check("bsa_rope_frequencies", _lib.bsa_rope_frequencies(
-        int(n_pairs), float(base), ROPE_SCALINGS[scaling], float(factor), float(original_length),
+        n_pairs, float(base), ROPE_SCALINGS[scaling], float(factor), float(original_length),
         float(beta_fast), float(beta_slow), out.ctypes.data_as(ctypes.c_void_p),
         ctypes.byref(amp)))
-    return out[:int(n_pairs)], float(amp.value)
+    return out[:n_pairs], float(amp.value)
 
 
 def bsa_rope_phases(freqs) -> np.ndarray:
@@ -716,7 +731,7 @@ class Rope:
     def __init__(self, pairs, layout: str = "interleaved", base: float = 10000.0,
                  scaling: str = "none", factor: float = 1.0, original_length: float = 1.0,
                  beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
-        pairs = tuple(int(p) for p in pairs)
+        pairs = tuple(_whole(p) for p in pairs)
         made = [bsa_rope_frequencies(p, base, scaling, factor, original_length, beta_fast,
                                      beta_slow) for p in pairs if p > 0]
         if not made:
@@ -732,7 +747,7 @@ class Rope:
         return self
 
     def _set(self, freqs, pairs, layout, amplitude, device):
-        pairs = tuple(int(p) for p in pairs)
+        pairs = tuple(_whole(p) for p in pairs)
         if len(pairs) not in (1, 3) or min(pairs) < 0:
             raise ValueError("pairs must be (P,) or (Pt, Ph, Pw)")
         if layout not in ROPE_LAYOUTS:
@@ -760,11 +775,15 @@ class Rope:
         if pos is not None:
             c.pos = pos.data_ptr()
         c.inverse = int(bool(inverse))
-        o0, o1, o2 = origin
+        origin = tuple(origin)
+        at = tuple(map(int, origin))
+        if at != origin:
+            raise TypeError("origin must be three whole positions")
+        o0, o1, o2 = at
         for x in (o0, o1, o2):
             if not -(1 << 31) <= x < (1 << 31):
                 raise ValueError("origin must be three int32 positions")
-        c.origin[0], c.origin[1], c.origin[2] = int(o0), int(o1), int(o2)
+        c.origin[0], c.origin[1], c.origin[2] = o0, o1, o2
         return c
 
 
@@ -816,6 +835,7 @@ def bsa_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope: Rope,
     n tokens is T = n, H = W = 1.  ``pos`` (int32 [axes, B, T*H*W]) gives every
     token's positions, otherwise the grid does; ``origin`` is added to both.
     ``inverse`` turns back: the gradient of the call.  ``out`` may be x_tok."""
+    T, H, W = _chunk(T, H, W)
     B, N, Hh, D = _tokens_shape(x_tok, "x_tok", T, H, W)
     dev = x_tok.device
     if out is None:
@@ -824,7 +844,7 @@ def bsa_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope: Rope,
         _need(out, "out", torch.bfloat16, dev, x_tok.shape)
     if rope is None:
         raise TypeError("rope must be a Rope")
-    _on(dev, "bsa_rope", _ptr(x_tok), _ptr(out), B, Hh, D, int(T), int(H), int(W),
+    _on(dev, "bsa_rope", _ptr(x_tok), _ptr(out), B, Hh, D, T, H, W,
         _rope_struct(rope, dev, B, N, pos, origin, inverse), _stream(dev))
     return out
 
@@ -837,6 +857,7 @@ def bsa_tokens_to_blocks_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope:
     """bsa_tokens_to_blocks of the turned tokens in one pass; returns the blocks,
     or (blocks, means) with ``want_mean`` or a ``mean`` buffer.  ``perm`` (int32
     [T*H*W], token -> slot) replaces the Gilbert order."""
+    T, H, W = _chunk(T, H, W)
     B, N, Hh, D = _tokens_shape(x_tok, "x_tok", T, H, W)
     dev = x_tok.device
     nb = n_blocks_for(T, H, W)
@@ -851,8 +872,8 @@ def bsa_tokens_to_blocks_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope:
     if rope is None:
         raise TypeError("rope must be a Rope")
     table = _perm_or_gilbert(perm, T, H, W, dev)
-    _on(dev, "bsa_tokens_to_blocks_rope", _ptr(x_tok), _ptr(out), _ptr(mean), B, Hh, D, int(T),
-        int(H), int(W), _ptr(table), _rope_struct(rope, dev, B, N, pos, origin),
+    _on(dev, "bsa_tokens_to_blocks_rope", _ptr(x_tok), _ptr(out), _ptr(mean), B, Hh, D, T, H, W,
+        _ptr(table), _rope_struct(rope, dev, B, N, pos, origin),
         _ptr(error_word(dev)), _stream(dev))
     return out if mean is None else (out, mean)
 
@@ -861,6 +882,7 @@ def bsa_kv_append_rope(cache: KVCache, k_tok: torch.Tensor, v_tok: torch.Tensor,
                        W: int, rope: Rope, pos: Optional[torch.Tensor] = None, origin=(0, 0, 0),
                        perm: Optional[torch.Tensor] = None) -> int:
     """bsa_kv_append with the keys turned on the way; returns the first block."""
+    T, H, W = _chunk(T, H, W)
     dev = cache.device
     shape = (cache.B, T * H * W, cache.Hh, cache.D)
     _need(k_tok, "k_tok", torch.bfloat16, dev, shape)
@@ -870,8 +892,8 @@ def bsa_kv_append_rope(cache: KVCache, k_tok: torch.Tensor, v_tok: torch.Tensor,
     table = _perm_or_gilbert(perm, T, H, W, dev)
     cs = cache.c_struct()
     first = cache.n_blocks
-    _on(dev, "bsa_kv_append_rope", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), int(T), int(H),
-        int(W), _ptr(table), _rope_struct(rope, dev, cache.B, T * H * W, pos, origin),
+    _on(dev, "bsa_kv_append_rope", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), T, H, W,
+        _ptr(table), _rope_struct(rope, dev, cache.B, T * H * W, pos, origin),
         _ptr(error_word(dev)), _stream(dev))
     cache.n_blocks = int(cs.n_blocks)
     return first
@@ -950,6 +972,7 @@ def bsa_kv8_append(cache: KVCache8, k_tok: torch.Tensor, v_tok: torch.Tensor, T:
     """Append one chunk (bf16 [B, T*H*W, Hh, D] K and V) to an 8-bit cache, the keys
     turned on the way when ``rope`` is given; returns its first block."""
     _need_cache8(cache)
+    T, H, W = _chunk(T, H, W)
     dev = cache.device
     shape = (cache.B, T * H * W, cache.Hh, cache.D)
     _need(k_tok, "k_tok", torch.bfloat16, dev, shape)
@@ -957,7 +980,7 @@ def bsa_kv8_append(cache: KVCache8, k_tok: torch.Tensor, v_tok: torch.Tensor, T:
     table = _perm_or_gilbert(perm, T, H, W, dev)
     cs = cache.c_struct8()
     first = cache.n_blocks
-    _on(dev, "bsa_kv8_append", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), int(T), int(H), int(W),
+    _on(dev, "bsa_kv8_append", ctypes.byref(cs), _ptr(k_tok), _ptr(v_tok), T, H, W,
         _ptr(table), _rope_struct(rope, dev, cache.B, T * H * W, pos, origin),
         _ptr(error_word(dev)), _stream(dev))
     cache.n_blocks = int(cs.n_blocks)

@@ -5,6 +5,7 @@ import math
 
 import numpy as np
 import pytest
+import torch
 
 import block_sparse_kv_bsa_b200 as bsa
 
@@ -176,3 +177,25 @@ def test_decode_workspace_covers_every_smaller_route():
         bsa.bsa_kv8_attn_decode_workspace_size(1, 3, 2, 128, 1, 10)
     with pytest.raises(bsa.BsaError):
         bsa.bsa_kv8_attn_decode_workspace_size(1, 2, 2, 96, 1, 10)
+
+
+def test_rope_handle_refuses_fractions():
+    # Positions and counts are whole numbers: a fraction is refused, not cut off.
+    handle = bsa.Rope((4, 2, 2), device="cpu")
+    for origin in ((0.5, 0, 0), (0, -1.25, 0), (0, 0, np.float32(3.9)), ("1", 0, 0)):
+        with pytest.raises(TypeError):
+            handle.c_struct(1, 8, None, origin)
+    got = handle.c_struct(1, 8, None, (np.int64(-7), 5.0, 188))
+    assert list(got.origin) == [-7, 5, 188]
+    with pytest.raises(ValueError):
+        handle.c_struct(1, 8, None, (0, 1 << 31, 0))
+    with pytest.raises(TypeError):
+        bsa.Rope((4.5, 2, 2), device="cpu")
+    with pytest.raises(TypeError):
+        bsa.Rope.from_frequencies([1.0, 0.5], (2.9,), device="cpu")
+    with pytest.raises(TypeError):
+        bsa.bsa_rope_frequencies(2.5)
+    x = torch.zeros((1, 5, 2, 64), dtype=torch.bfloat16)
+    for call in (bsa.bsa_rope, bsa.bsa_tokens_to_blocks_rope):
+        with pytest.raises(TypeError, match="whole"):
+            call(x, 2.5, 2, 1, handle)
