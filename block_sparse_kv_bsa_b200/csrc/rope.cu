@@ -298,7 +298,9 @@ bsa_status check_rope_chunk(int B, int Hh, int D, int T, int H, int W) {
   if (D != 64 && D != 128) return BSA_ERR_UNSUPPORTED;
   const long long plane = static_cast<long long>(T) * H;
   if (plane > (1LL << 24) || plane * W > (1LL << 24)) return BSA_ERR_SHAPE;
-  if (B > 32767 || Hh > 65535) return BSA_ERR_SHAPE;
+  if (B > 65535 || Hh > 65535) return BSA_ERR_SHAPE;  // grid limits of the means and bsa_rope
+  const long long nb = (plane * W + kBlk - 1) / kBlk;
+  if (nb * B * Hh >= (1LL << 31)) return BSA_ERR_SHAPE;  // tiles are counted in 32 bits
   return BSA_OK;
 }
 

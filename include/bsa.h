@@ -511,7 +511,8 @@ bsa_status bsa_rope_phases(const double *host_freq, int n, int64_t *host_phase);
  *   y_tok  device bf16, the same shape; may be x_tok (in place), and must not
  *          overlap it otherwise
  * Errors: BSA_ERR_INVALID_ARG, BSA_ERR_SHAPE (B or Hh above 65535, T*H*W
- *         above 2^24), BSA_ERR_UNSUPPORTED (D), BSA_ERR_CUDA.
+ *         above 2^24, B * Hh * ceil(T*H*W / 128) not below 2^31),
+ *         BSA_ERR_UNSUPPORTED (D), BSA_ERR_CUDA.
  */
 bsa_status bsa_rope(const void *x_tok, void *y_tok, int B, int Hh, int D, int T, int H, int W,
                     const bsa_rope_desc *rope, void *stream);

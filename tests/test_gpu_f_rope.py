@@ -231,3 +231,27 @@ def test_offsets_past_32_bits():
     part = bsa.bsa_tokens_to_blocks_rope(x[B - 1:], T, H, W, rope)
     assert torch.equal(blk[B - 1:], part)
     bsa.raise_on_device_error(DEV)
+
+
+def test_batches_up_to_the_stated_limit():
+    # 65535 batch entries: the last ones give the bits of a call on those alone.
+    B, N, D, last = 65535, 3, 64, 2
+    x, v = tokens(B, N, 1, D, 71), tokens(B, N, 1, D, 72)
+    _, rope = make((16, 8, 8), "half")
+    part, vpart = x[-last:].contiguous(), v[-last:].contiguous()
+    y = bsa.bsa_rope(x, 1, 1, N, rope, origin=(5, 0, 0))
+    assert torch.equal(y[-last:], bsa.bsa_rope(part, 1, 1, N, rope, origin=(5, 0, 0)))
+    blk, mean = bsa.bsa_tokens_to_blocks_rope(x, 1, 1, N, rope, want_mean=True)
+    want = bsa.bsa_tokens_to_blocks_rope(part, 1, 1, N, rope, want_mean=True)
+    assert torch.equal(blk[-last:], want[0]) and torch.equal(mean[-last:], want[1])
+    del blk, mean
+    for kind, append in ((bsa.KVCache, bsa.bsa_kv_append_rope), (bsa.KVCache8, bsa.bsa_kv8_append)):
+        whole = kind(B, 1, D, 1, device=DEV, pooled_keys=True)
+        few = kind(last, 1, D, 1, device=DEV, pooled_keys=True)
+        append(whole, x, v, 1, 1, N, rope)
+        append(few, part, vpart, 1, 1, N, rope)
+        for name in ("k", "v", "kmean"):
+            a, b = (getattr(c, name).view(torch.uint8) for c in (whole, few))
+            assert torch.equal(a[-last:], b), name
+        del whole, few
+    bsa.raise_on_device_error(DEV)

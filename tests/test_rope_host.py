@@ -199,3 +199,16 @@ def test_rope_handle_refuses_fractions():
     for call in (bsa.bsa_rope, bsa.bsa_tokens_to_blocks_rope):
         with pytest.raises(TypeError, match="whole"):
             call(x, 2.5, 2, 1, handle)
+
+
+@pytest.mark.parametrize("B,Hh,T,status", [(65536, 1, 1, SHAPE), (1, 65536, 1, SHAPE),
+                                           (65535, 65535, 1, SHAPE),
+                                           (40000, 4, 1 << 24, SHAPE)])
+def test_rotated_calls_refuse_sizes_past_their_limits(B, Hh, T, status):
+    lib, d = bsa.lib(), rope()
+    at = ctypes.byref(d)
+    assert lib.bsa_rope(A16, A16, B, Hh, 64, T, 1, 1, at, None) == status
+    assert lib.bsa_tokens_to_blocks_rope(A16, A16, None, B, Hh, 64, T, 1, 1, None, at, None,
+                                         None) == status
+    c = cache8(B=B, Hh=Hh)
+    assert lib.bsa_kv8_append(ctypes.byref(c), A16, A16, T, 1, 1, None, at, None, None) == status
