@@ -855,7 +855,8 @@ def bsa_tokens_to_blocks_rope(x_tok: torch.Tensor, T: int, H: int, W: int, rope:
                               mean: Optional[torch.Tensor] = None, want_mean: bool = False,
                               perm: Optional[torch.Tensor] = None):
     """bsa_tokens_to_blocks of the turned tokens in one pass; returns the blocks,
-    or (blocks, means) with ``want_mean`` or a ``mean`` buffer.  ``perm`` (int32
+    or (blocks, means) with ``want_mean`` or a ``mean`` buffer (the means by a second
+    kernel).  ``perm`` (int32
     [T*H*W], token -> slot) replaces the Gilbert order."""
     T, H, W = _chunk(T, H, W)
     B, N, Hh, D = _tokens_shape(x_tok, "x_tok", T, H, W)
@@ -993,7 +994,8 @@ def bsa_kv8_attn(q_blk: torch.Tensor, cache: KVCache8, idx: torch.Tensor, cnt: t
                  ) -> Tuple[torch.Tensor, torch.Tensor]:
     """bsa_attn over an 8-bit cache: q_blk bf16 [B, Hq, nQB*128, D] with Hq a multiple
     of the cache's Hh, one route per cache head (idx [B, Hh, nQB, max_sel], cnt [B,
-    Hh, nQB]); returns (O like q_blk, LSE fp32 [B, Hq, nQB*128])."""
+    Hh, nQB]); returns (O like q_blk, LSE fp32 [B, Hq, nQB*128]).  For grouped heads,
+    bsa_route_qmean takes the query means averaged over each group."""
     _need_cache8(cache)
     dev = cache.device
     if q_blk.dim() != 4:

@@ -6,7 +6,12 @@
 // Both kernels are HBM streams: every element is read and written once (4
 // bytes).  A thread owns a slot of a token (rope.cuh), computes its eight angles
 // once and applies them to a run of heads, so the sines cost nothing per head
-// and no table goes through memory.
+// and no table goes through memory.  Not so the half layout with a pair count that
+// is no multiple of 8 (kRopeHalfAny): it computes an angle for every element of
+// every head and loads elements one by one; 7800 x 24 x 128 with 61 pairs takes
+// 125 us, with 56 or 64 pairs 22 to 25.  Means, where asked for, are a second
+// kernel over the blocks written (7800 x 24 x 128: 26.6 -> 34.8 us for one
+// tensor, 38.9 -> 49.2 us for K and V, cold L2).
 //   tokens  40001 x 24 heads x 64, 48 of 64 dimensions: 44.5 us, 5.5 TB/s
 //           (runs of 12 heads; runs of 24, one wave and a half of CTAs: 57 us)
 //   blocks  K and V of 7800 x 24 heads x 128: 36 us, 5.3 TB/s.  A CTA's start

@@ -456,7 +456,9 @@ bsa_status bsa_route_noalloc(const void *q_blk, const bsa_kv_cache *cache, const
  *   inverse    nonzero: turn by -theta.  With the same amplitude this is the
  *              transposed map: applied to the gradient of the turned
  *              tensor it gives the gradient of the tensor.
- * Arithmetic is fp32, rounded once to the output type.
+ * Arithmetic is fp32, rounded once to the output type.  BSA_ROPE_HALF with P
+ * not a multiple of 8 takes a slower form (angles and two-byte loads for every
+ * element of every head): five to eight times the time of the others.
  */
 #define BSA_ROPE_INTERLEAVED 0
 #define BSA_ROPE_HALF 1
@@ -519,10 +521,11 @@ bsa_status bsa_rope(const void *x_tok, void *y_tok, int B, int Hh, int D, int T,
 
 /*
  * bsa_tokens_to_blocks (or, with x_mean, bsa_tokens_to_blocks_mean) of the
- * turned tokens, in one pass: x_blk holds the turned values rounded to bf16,
- * x_mean (device fp32 [B, Hh, nb, D], 16-byte aligned, or NULL) the means of
- * the rounded rows, in the library's fixed order.  With a table (d_perm),
- * chunks of up to 16384 tokens; without one, up to 2^24.
+ * turned tokens: x_blk holds the turned values rounded to bf16, x_mean (device
+ * fp32 [B, Hh, nb, D], 16-byte aligned, or NULL) the means of the rounded
+ * rows, in the library's fixed order.  Turn and move are one pass; the means
+ * are pooled from x_blk by a second kernel.  With a table (d_perm), chunks of
+ * up to 16384 tokens; without one, up to 2^24.
  * Errors: those of bsa_rope and bsa_tokens_to_blocks; BSA_ERR_UNSUPPORTED
  *         above 16384 tokens with a table.
  */
@@ -533,7 +536,8 @@ bsa_status bsa_tokens_to_blocks_rope(const void *x_tok, void *x_blk, float *x_me
 /*
  * bsa_kv_append with the keys turned on the way into the cache (V is moved
  * as it is).  cache->kmean, when present, gets the means of the turned keys
- * as stored.  Chunk sizes as for bsa_tokens_to_blocks_rope.
+ * as stored, from a second kernel that reads them back.  Chunk sizes as for
+ * bsa_tokens_to_blocks_rope.
  * Errors: those of bsa_kv_append and bsa_tokens_to_blocks_rope.
  */
 bsa_status bsa_kv_append_rope(bsa_kv_cache *cache, const void *k_tok, const void *v_tok, int T,
@@ -584,7 +588,9 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
 /*
  * bsa_attn over an 8-bit cache, with grouped heads: Hq query heads, a
  * multiple of the cache's Hh; query head h reads cache head h / (Hq / Hh) and
- * that head's route.  Products run on the tensor core with fp32 accumulation;
+ * that head's route.  The route calls take queries, or query means, of the
+ * cache's head count: to route grouped heads, give bsa_route_qmean the mean over
+ * each group.  Products run on the tensor core with fp32 accumulation;
  * codes and bf16 queries enter them exactly (query elements below 2^-13 of
  * their row's largest with an error of at most 2^-21 of it), and the softmax
  * weights are rounded to f16.
@@ -599,8 +605,9 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
  * product is rounded by 2^-11 of itself, but by 2^-32 of the row's largest where
  * it is 2^21 or more below that, so beside a block of far larger value scale the
  * values of another keep only that absolute accuracy.
- * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh;
- *         on the device also BSA_DEV_BAD_SCALE.
+ * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh, or
+ *         B * Hq * n_q_blocks * 128 or B * Hh * max_blocks * 128 is not below
+ *         2^31; on the device also BSA_DEV_BAD_SCALE.
  */
 bsa_status bsa_kv8_attn(const void *q_blk, const bsa_kv_cache8 *cache, int Hq,
                         const int32_t *q_valid, const int32_t *idx, const int32_t *cnt,
@@ -617,7 +624,8 @@ bsa_status bsa_kv8_attn_decode_workspace_size(int B, int Hq, int Hh, int D, int 
  * The form for single tokens: n_tok query tokens (1 upward, n_tok * Hq / Hh
  * at most 128) of every batch entry attend over the blocks of one route per
  * cache head, or over the whole cache.  The keys are split over the GPU and
- * the parts joined by a second kernel, in a fixed order.
+ * the parts joined by a second kernel, in a fixed order.  Each 16 query rows of
+ * a cache head read its blocks for themselves.
  *   q_tok    device bf16 [B, n_tok, Hq, D]
  *   idx,cnt  device int32 [B, Hh, max_sel], [B, Hh], or both NULL: every
  *            block in use, [0, n_blocks) (max_sel is then not read)
@@ -627,7 +635,8 @@ bsa_status bsa_kv8_attn_decode_workspace_size(int B, int Hq, int Hh, int D, int 
  *   workspace  device, at least bsa_kv8_attn_decode_workspace_size bytes,
  *              256-aligned; calls that may overlap need one each
  * Errors: those of bsa_kv8_attn; BSA_ERR_CAPACITY (workspace too small);
- *         BSA_ERR_UNSUPPORTED (more than 128 query rows per cache head).
+ *         BSA_ERR_UNSUPPORTED (more than 128 query rows per cache head);
+ *         BSA_ERR_SHAPE also for B * Hh above 2^20 or max_sel above 2^30.
  */
 bsa_status bsa_kv8_attn_decode(const void *q_tok, const bsa_kv_cache8 *cache, int Hq, int n_tok,
                                const int32_t *idx, const int32_t *cnt, int max_sel,
