@@ -603,8 +603,9 @@ bsa_status bsa_kv8_append(bsa_kv_cache8 *cache, const void *k_tok, const void *v
  * within fp32's range, and value scales of one route within a factor of 2^100
  * of each other.  Weights are held in f16 times their block's value scale: such a
  * product is rounded by 2^-11 of itself, but by 2^-32 of the row's largest where
- * it is 2^21 or more below that, so beside a block of far larger value scale the
- * values of another keep only that absolute accuracy.
+ * it is 2^21 or more below that.  Values under a far smaller weight, or in a block
+ * of far smaller value scale, keep only that absolute accuracy, which shows in
+ * elements where the values that dominate the row are zero.
  * Errors: those of bsa_attn; BSA_ERR_SHAPE when Hq is not a multiple of Hh, or
  *         B * Hq * n_q_blocks * 128 or B * Hh * max_blocks * 128 is not below
  *         2^31; on the device also BSA_DEV_BAD_SCALE.
